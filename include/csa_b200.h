@@ -423,6 +423,144 @@ csa_status_t hca_dense_attn_at(const void* q, int dt, int B, int n_q, int H, int
                                int q_pos0, float softmax_scale, void* out, float* lse_out,
                                void* stream);
 
+/*
+ * csa_rope -- rotary positions of the tensors around the attention calls.
+ * "DeepSeek V4 CSA + CP 迁移到 HP：困难点深度分析" names them (the config fields
+ * qk_pos_emb_head_dim and rotary_interleaved: a part of each head is rotated)
+ * without a formula; this is the reading.  For the token at position p, pair j
+ * of the d_rot rotated channels of every head turns by the angle p * freqs[j]:
+ *     (a, b) -> scale * (a cos - b sin, b cos + a sin)
+ *   interleaved = 1: a, b = channels rot_offset + 2j and + 2j + 1
+ *   interleaved = 0: a, b = channels rot_offset + j and + j + d_rot/2
+ *   transpose = 1: the angle's sign flips -- the gradient of the rotation, and,
+ *     for scale = 1, its inverse (shared KV: a rotated row is also the value, so
+ *     an attention output is turned back by the query's position).
+ * The other channels are passed on unchanged.  A token with a negative
+ * position has no place in the sequence: its heads are passed on unrotated.
+ * Rotation runs in fp32 from angles exact to 2^-31 of a turn at any position,
+ * and is rounded once.
+ *
+ *   x, y   up to two tensors with D channels a head, H and H_y heads a token
+ *          (query heads and the KV row, say), rotated in one launch; H or H_y
+ *          = 0: no such tensor.  Channels are contiguous.
+ *   x_strides  HOST long long [4], in elements: token and head stride of x, token
+ *          and head stride of x_out (token b * n + j starts at (b * n + j) times
+ *          the token stride); NULL: both contiguous [B, n, H, D].  Strides may
+ *          be any non-negative numbers, but output heads and tokens must not overlap.
+ *   x_out  may be x (with the same strides; then only the rotated channels are
+ *          written); otherwise it must not overlap x or y.
+ *   dt     CSA_DT_F32 or CSA_DT_BF16, of every tensor.
+ *   freqs  HOST double [d_rot / 2], radians a position (see csa_rope_freqs),
+ *          |freqs| <= 10^6; read before the call returns.
+ *   pos    device int32 [B, n], or NULL: token j of every element sits at
+ *          pos0 + j * pos_step (pos0, pos_step >= 0; a compressed cache's entries
+ *          by pos_step = m).
+ *   Limits: d_rot even, 2 <= d_rot <= 256, rot_offset + d_rot <= D <= 4096,
+ *          H, H_y <= 4096, B * n < 2^31.
+ */
+csa_status_t csa_rope(const void* x, void* x_out, int H, const long long* x_strides,
+                      const void* y, void* y_out, int H_y, const long long* y_strides, int dt,
+                      int B, int n, int D, int d_rot, int rot_offset, int interleaved,
+                      const double* freqs, float scale, const int* pos, int pos0, int pos_step,
+                      int transpose, void* stream);
+
+/*
+ * csa_rope_freqs -- frequencies for csa_rope, scaled for contexts longer than
+ * the trained one (host only, no launch).
+ *   f_j = base^(-2j / d_rot); factor = 1: freqs[j] = f_j, scale = 1.
+ *   factor > 1 (the YaRN rule: Peng et al., "YaRN: Efficient Context Window
+ *   Extension of Large Language Models", 2023, with the ramp over the pair
+ *   index): pairs that turn more than beta_fast times within original_len
+ *   positions keep f_j, those below beta_slow turns get f_j / factor, a linear
+ *   ramp joins them:
+ *     pair(r) = d_rot ln(original_len / (2 pi r)) / (2 ln base)
+ *     lo = max(floor(pair(beta_fast)), 0), hi = min(ceil(pair(beta_slow)), d_rot - 1)
+ *     g_j = clamp((j - lo) / (hi - lo), 0, 1)      (hi - lo: at least 0.001)
+ *     freqs[j] = g_j f_j / factor + (1 - g_j) f_j,  scale = 0.1 ln(factor) + 1
+ *   freqs  HOST double [d_rot / 2];  scale  HOST float or NULL.
+ */
+csa_status_t csa_rope_freqs(int d_rot, double base, double factor, int original_len,
+                            double beta_fast, double beta_slow, double* freqs, float* scale);
+
+/*
+ * hca_dense_attn_prefix -- HCA for a batch whose elements share a long prefix.
+ * The first N_p compressed entries of every element are the same (one system
+ * prompt or document, many users) and stored once:
+ *   logical entry i of element b is  kv_p[i]            for i < N_p,
+ *                                    kv_c[b, i - N_p]   for N_p <= i < N_p + N_cap;
+ *   n_entries [B] counts logical entries, prefix included (NULL: N_p + N_cap).
+ * The result is that of hca_dense_attn over the logical caches (the serving
+ * counterpart of "DS-V4 分析&学习" §1.4; sharing is this library's addition).
+ *   kv_p  [N_p, D]   kv_c  [B, N_cap, D]   (either may have no rows)
+ *   workspace  device memory of at least hca_dense_attn_prefix_workspace(...)
+ *     bytes, on a 16-byte boundary (may be NULL where that is 0).  Its contents
+ *     mean nothing before or after the call; calls that can run at the same time
+ *     (two streams, two graphs) each need one of their own.
+ *   Rows at a negative position see no key: out = 0, lse = -inf.
+ *   Every other argument, the limits and the errors are those of
+ *   hca_dense_attn; a workspace that is too small is CSA_ERR_INVALID_ARG.
+ *   Heads x dims: H in {8, 16, 32, 64, 128}, D in {64, 128}.
+ */
+unsigned long long hca_dense_attn_prefix_workspace(int dt, int B, int n_q, int H, int D, int N_p,
+                                                   int N_cap, int window);
+
+csa_status_t hca_dense_attn_prefix(const void* q, int dt, int B, int n_q, int H, int D,
+                                   const void* kv_p, int N_p, const void* kv_c, int N_cap,
+                                   const int* n_entries, int m, const void* kv_raw, int L_raw,
+                                   const int* raw_pos0, const int* raw_len, int window,
+                                   const int* q_pos, float softmax_scale, void* out,
+                                   float* lse_out, void* workspace,
+                                   unsigned long long workspace_bytes, void* stream);
+
+/*
+ * hca_entry_weights -- the attention weight each compressed entry received.
+ *   weight_out[b, s] = weight_in[b, s]
+ *       + sum_{q, h} exp(softmax_scale * q[b, q, h] . kv_c[b, s] - lse[b, q, h])
+ * over the query rows q that see s and all heads, with the lse that the
+ * attention call of those rows wrote (so a head's weights over all its keys,
+ * window included, add to one).  A user accumulates them over decode steps and
+ * passes them to csa_evict.  (The pages keep every entry; accumulating and
+ * evicting are this library's addition for caches of a fixed budget.)
+ *   A row at position t sees s < min(floor((t+1)/m), n_entries[b]) (as
+ *   hca_dense_attn); a row whose lse is -inf adds nothing.
+ *   idx  [B, topk] int32: only the listed entries receive weight (the lists that
+ *     csa_evict wrote and csa_sparse_attn attended to; negative values and
+ *     values >= N_cap are skipped, an entry listed twice receives it twice);
+ *     NULL: every visible entry.  The other entries keep what they had.
+ *   q [B, n_q, H, D], kv_c [B, N_cap, D]: dt CSA_DT_F32 or CSA_DT_BF16.
+ *   lse [B, n_q, H] fp32;  q_pos [B, n_q] (NULL: q);  n_entries [B] (NULL: N_cap).
+ *   weight_in [B, N_cap] fp32 or NULL (zeros); it may be weight_out, and must not
+ *     overlap it otherwise.  weight_out [B, N_cap] fp32.
+ *   Products and sums are fp32.  softmax_scale <= 0 selects 1/sqrt(D).
+ *   Limits: D a multiple of 16 and <= 256, H >= 1.
+ */
+csa_status_t hca_entry_weights(const void* q, int dt, int B, int n_q, int H, int D,
+                               const void* kv_c, int N_cap, const int* idx, int topk,
+                               const int* n_entries, int m, const int* q_pos,
+                               float softmax_scale, const float* lse, const float* weight_in,
+                               float* weight_out, void* stream);
+
+/*
+ * csa_evict -- which entries a cache of `budget` entries keeps.
+ * Candidates of element b: s < n_entries[b] with weight[b, s] >= 0 (a negative
+ * weight marks an entry evicted before; NaN counts as evicted).  The candidates
+ * among the newest `recent` positions (s >= n_entries[b] - recent) come first,
+ * newest first, then the others by weight, largest first, equal weights lowest
+ * index first; the first `budget` are kept.
+ *   idx_out  [B, budget] int32: the kept entries in ascending order, then -1: a
+ *     row that csa_sparse_attn takes as idx (one query row an element, budget
+ *     <= 2048) and hca_entry_weights as its list.
+ *   n_kept   [B] int32 or NULL: how many were kept.
+ *   weight   [B, N_cap] fp32, updated: every entry s < n_entries[b] that is not
+ *     kept gets -1, so a later call does not keep it; kept entries and those
+ *     behind n_entries[b] stay as they are.  An entry appended later starts at
+ *     weight 0 (a buffer zeroed when it is allocated).
+ *   n_entries  [B] device int32 (NULL: N_cap).
+ * The caches themselves are not touched.
+ */
+csa_status_t csa_evict(float* weight, int B, int N_cap, const int* n_entries, int budget,
+                       int recent, int* idx_out, int* n_kept, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

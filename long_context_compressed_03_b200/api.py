@@ -8,7 +8,8 @@ in the library's kernels; there is no fallback of any kind -- if the library
 is missing or fails to load, the first call raises.
 
 Convenience wrappers (``compress``, ``indexer_topk``, ``sparse_attn``,
-``hca_attn``, ``csa_prefill``) allocate their outputs with ``torch.empty``
+``hca_attn``, ``csa_prefill``, ``rope``, ``hca_attn_prefix``, ``entry_weights``,
+``evict``) allocate their outputs with ``torch.empty``
 and call the ABI functions.
 """
 from __future__ import annotations
@@ -29,6 +30,7 @@ DT_F32, DT_BF16, DT_E4M3, DT_E4M3_HADAMARD = 0, 1, 2, 3
 
 # symbol -> (restype, argtypes); mirrors include/csa_b200.h
 P, I, F = ctypes.c_void_p, ctypes.c_int, ctypes.c_float
+DBL, U64 = ctypes.c_double, ctypes.c_ulonglong
 SIGNATURES = {
     "csa_status_string": (ctypes.c_char_p, [I]),
     "csa_last_error_detail": (ctypes.c_char_p, []),
@@ -57,6 +59,13 @@ SIGNATURES = {
     "csa_indexer_topk_at": (I, [P, I, P, P, P, I, P, I, I, I, I, I, P, I, I, I, P, P]),
     "csa_sparse_attn_at": (I, [P, I, I, I, I, I, P, I, P, I, P, I, I, I, I, F, P, P, P]),
     "hca_dense_attn_at": (I, [P, I, I, I, I, I, P, I, P, I, P, I, I, I, I, F, P, P, P]),
+    "csa_rope": (I, [P, P, I, P, P, P, I, P, I, I, I, I, I, I, I, P, F, P, I, I, I, P]),
+    "csa_rope_freqs": (I, [I, DBL, DBL, I, DBL, DBL, P, P]),
+    "hca_dense_attn_prefix_workspace": (U64, [I, I, I, I, I, I, I, I]),
+    "hca_dense_attn_prefix": (I, [P, I, I, I, I, I, P, I, P, I, P, I, P, I, P, P, I, P, F, P, P, P,
+                                  U64, P]),
+    "hca_entry_weights": (I, [P, I, I, I, I, I, P, I, P, I, P, I, P, F, P, P, P, P]),
+    "csa_evict": (I, [P, I, I, P, I, I, P, P, P]),
 }
 
 
@@ -445,6 +454,185 @@ def hca_dense_attn_paged(q: torch.Tensor, kv_c: PagedCache, m: int, kv_raw: torc
         _stream(stream)))
 
 
+# ---------------------------------------------------------------- rotary positions
+def _same_device(t: torch.Tensor) -> None:
+    """The library launches on the current device: refuse tensors of another one."""
+    if t.is_cuda and t.device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {t.device}, but the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+
+
+def _shape(t: torch.Tensor | None, shape: tuple, name: str, dtype=None):
+    """Checks a tensor's shape (and dtype), then passes its pointer."""
+    if t is not None:
+        if tuple(t.shape) != shape:
+            raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
+        if dtype is not None and t.dtype != dtype:
+            raise ValueError(f"{name} must be {dtype}")
+    return _ptr(t)
+
+
+def rope_freqs(d_rot: int, base: float = 10000.0, factor: float = 1.0, original_len: int = 0,
+               beta_fast: float = 32.0, beta_slow: float = 1.0) -> tuple[torch.Tensor, float]:
+    """Frequencies (float64, on the host, radians a position) of the rotated
+    pairs and the scale of cos and sin; ``factor`` > 1 applies the YaRN rule for
+    contexts ``factor`` times ``original_len``."""
+    freqs = torch.empty(max(d_rot // 2, 1), dtype=torch.float64)
+    scale = ctypes.c_float()
+    _check(load().csa_rope_freqs(d_rot, base, factor, original_len, beta_fast, beta_slow,
+                                 freqs.data_ptr(), ctypes.addressof(scale)))
+    return freqs, scale.value
+
+
+_STRIDES = ctypes.c_longlong * 4
+
+
+def _rope_tensor(x: torch.Tensor | None, out: torch.Tensor | None, dims: tuple, name: str):
+    """(x, out, heads, strides) arguments of csa_rope for one tensor [B, n, H, D]."""
+    if x is None:
+        if out is not None:
+            raise ValueError(f"an output for {name}, but no {name}")
+        return None, None, 0, None
+    if out is None:
+        raise ValueError(f"{name} needs an output")
+    B, n, D, dt = dims
+    if x.dim() != 4 or x.shape[0] != B or x.shape[1] != n or x.shape[3] != D or x.dtype != dt:
+        raise ValueError(f"{name} must be [B, n, heads, D], of one shape and dtype with the other tensor")
+    if out.shape != x.shape or out.dtype != x.dtype:
+        raise ValueError(f"the output of {name} must have its shape and dtype")
+    _same_device(x)
+    st = []
+    for t in (x, out):
+        if not t.is_cuda:
+            raise ValueError("tensor arguments must be CUDA tensors")
+        if t.is_contiguous():
+            st += [x.shape[2] * D, D]
+            continue
+        s0, s1, s2, s3 = t.stride()
+        if (D > 1 and s3 != 1) or (B > 1 and n > 0 and s0 != n * s1):
+            raise ValueError(f"{name}: channels must be contiguous and elements n tokens apart")
+        if n == 1 and B > 1:
+            s1 = s0
+        st += [s1, s2]
+    if out.data_ptr() != x.data_ptr() and x.numel():
+        # (ranges of the storage; views that interleave inside one buffer are refused too)
+        a0, b0, e = x.data_ptr(), out.data_ptr(), x.element_size()
+        a1 = a0 + ((B * n - 1) * st[0] + (x.shape[2] - 1) * st[1] + D) * e
+        b1 = b0 + ((B * n - 1) * st[2] + (x.shape[2] - 1) * st[3] + D) * e
+        if a0 < b1 and b0 < a1:
+            raise ValueError(f"the output of {name} overlaps it (give {name} itself to rotate in place)")
+    return x.data_ptr(), out.data_ptr(), x.shape[2], _STRIDES(*st)
+
+
+def csa_rope(x: torch.Tensor, x_out: torch.Tensor, freqs: torch.Tensor,
+             y: torch.Tensor | None = None, y_out: torch.Tensor | None = None,
+             pos: torch.Tensor | None = None, rot_offset: int = 0, interleaved: bool = True,
+             scale: float = 1.0, pos0: int = 0, pos_step: int = 1, transpose: bool = False,
+             stream=None) -> None:
+    """x [B, n, H, D] (and y [B, n, H_y, D]) rotated into x_out (y_out); the outputs may
+    be the inputs.  ``freqs``: float64 host tensor [d_rot / 2]; ``pos`` [B, n] int32, or
+    token j sits at pos0 + j * pos_step.  Views of a larger tensor are taken as long as
+    their channels are contiguous and their elements n tokens apart."""
+    if x.dim() != 4:
+        raise ValueError("x must be [B, n, heads, D]")
+    if freqs.dtype != torch.float64 or freqs.is_cuda or not freqs.is_contiguous() or freqs.dim() != 1:
+        raise ValueError("freqs must be a contiguous float64 host tensor [d_rot / 2]")
+    B, n, _, D = x.shape
+    dims = (B, n, D, x.dtype)
+    xa, xo, H, xs = _rope_tensor(x, x_out, dims, "x")
+    ya, yo, Hy, ys = _rope_tensor(y, y_out, dims, "y")
+    if pos is not None:
+        _i32(pos, "pos")
+    _check(load().csa_rope(xa, xo, H, xs, ya, yo, Hy, ys, _dt(x), B, n, D, 2 * freqs.numel(),
+                           rot_offset, int(bool(interleaved)), freqs.data_ptr(), scale,
+                           _shape(pos, (B, n), "pos"), pos0, pos_step, int(bool(transpose)),
+                           _stream(stream)))
+
+
+# ---------------------------------------------------------------- shared prefix
+def hca_dense_attn_prefix(q: torch.Tensor, kv_p: torch.Tensor, kv_c: torch.Tensor, m: int,
+                          kv_raw: torch.Tensor, window: int, out: torch.Tensor,
+                          lse_out: torch.Tensor | None = None,
+                          n_entries: torch.Tensor | None = None,
+                          raw_pos0: torch.Tensor | None = None,
+                          raw_len: torch.Tensor | None = None, q_pos: torch.Tensor | None = None,
+                          softmax_scale: float = 0.0, workspace: torch.Tensor | None = None,
+                          stream=None) -> None:
+    """hca_dense_attn over entries kv_p [N_p, D] (shared by the batch), then kv_c
+    [B, N_cap, D].  ``workspace``: a CUDA tensor of hca_dense_attn_prefix_workspace(...)
+    bytes; None takes one from torch's allocator, on the stream the call runs on."""
+    B, n_q, H, D = q.shape
+    _same_device(q)
+    if not (q.dtype == kv_p.dtype == kv_c.dtype == kv_raw.dtype == out.dtype):
+        raise ValueError("q, kv_p, kv_c, kv_raw and out must share one dtype")
+    N_p, N_cap, L = kv_p.shape[0], kv_c.shape[1], kv_raw.shape[1]
+    dt = _dt(q)
+    lib = load()
+    if workspace is None:
+        need = lib.hca_dense_attn_prefix_workspace(dt, B, n_q, H, D, N_p, N_cap, window)
+        if need:
+            workspace = _scratch(need, q.device, stream)
+    ws, wb = (workspace.data_ptr(), workspace.numel() * workspace.element_size()) \
+        if workspace is not None else (None, 0)
+    _check(lib.hca_dense_attn_prefix(
+        _ptr(q), dt, B, n_q, H, D, _shape(kv_p, (N_p, D), "kv_p"), N_p,
+        _shape(kv_c, (B, N_cap, D), "kv_c"), N_cap, _shape(n_entries, (B,), "n_entries", torch.int32),
+        m, _shape(kv_raw, (B, L, D), "kv_raw"), L, _shape(raw_pos0, (B,), "raw_pos0", torch.int32),
+        _shape(raw_len, (B,), "raw_len", torch.int32), window,
+        _shape(q_pos, (B, n_q), "q_pos", torch.int32), softmax_scale,
+        _shape(out, (B, n_q, H, D), "out"),
+        _shape(lse_out, (B, n_q, H), "lse_out", torch.float32), ws, wb, _stream(stream)))
+
+
+def _scratch(nbytes: int, device, stream) -> torch.Tensor:
+    """Device memory that lives until the work queued on ``stream`` so far is done."""
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+    with torch.cuda.stream(s):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+# ---------------------------------------------------------------- entry weights, eviction
+def hca_entry_weights(q: torch.Tensor, kv_c: torch.Tensor, m: int, lse: torch.Tensor,
+                      weight_out: torch.Tensor, weight_in: torch.Tensor | None = None,
+                      idx: torch.Tensor | None = None, n_entries: torch.Tensor | None = None,
+                      q_pos: torch.Tensor | None = None, softmax_scale: float = 0.0,
+                      stream=None) -> None:
+    """weight_out [B, N_cap] = weight_in (or 0) + the weight that each visible (or listed:
+    idx [B, topk]) entry of kv_c [B, N_cap, D] received from q [B, n_q, H, D], given the
+    attention's lse [B, n_q, H]."""
+    B, n_q, H, D = q.shape
+    _same_device(q)
+    if q.dtype != kv_c.dtype:
+        raise ValueError("q and kv_c must share one dtype")
+    N_cap = kv_c.shape[1]
+    topk = 0 if idx is None else idx.shape[-1]
+    _check(load().hca_entry_weights(
+        _ptr(q), _dt(q), B, n_q, H, D, _shape(kv_c, (B, N_cap, D), "kv_c"), N_cap,
+        _shape(idx, (B, topk), "idx", torch.int32), topk,
+        _shape(n_entries, (B,), "n_entries", torch.int32), m,
+        _shape(q_pos, (B, n_q), "q_pos", torch.int32), softmax_scale,
+        _shape(lse, (B, n_q, H), "lse", torch.float32),
+        _shape(weight_in, (B, N_cap), "weight_in", torch.float32),
+        _shape(weight_out, (B, N_cap), "weight_out", torch.float32), _stream(stream)))
+
+
+def csa_evict(weight: torch.Tensor, budget: int, idx_out: torch.Tensor,
+              n_kept: torch.Tensor | None = None, recent: int = 0,
+              n_entries: torch.Tensor | None = None, stream=None) -> None:
+    """weight [B, N_cap] fp32 (updated: evicted entries get -1) -> idx_out [B, budget]
+    int32, the kept entries in ascending order, then -1; n_kept [B] int32."""
+    if weight.dim() != 2:
+        raise ValueError("weight must be [B, N_cap]")
+    B, N_cap = weight.shape
+    _same_device(weight)
+    _check(load().csa_evict(_shape(weight, (B, N_cap), "weight", torch.float32), B, N_cap,
+                            _shape(n_entries, (B,), "n_entries", torch.int32), budget, recent,
+                            _shape(idx_out, (B, budget), "idx_out", torch.int32),
+                            _shape(n_kept, (B,), "n_kept", torch.int32), _stream(stream)))
+
+
 # ---------------------------------------------------------------- allocating wrappers
 def compress(x: torch.Tensor, W: torch.Tensor, m: int, overlap: bool, out_dtype=None,
              hadamard: bool = False, stream=None):
@@ -503,6 +691,36 @@ def hca_attn(q, kv_c, m: int, kv_raw, window: int, with_lse: bool = False, **kw)
     lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device) if with_lse else None
     hca_dense_attn(q, kv_c, m, kv_raw, window, out, lse_out=lse, **kw)
     return (out, lse) if with_lse else out
+
+
+def rope(x, freqs, pos=None, y=None, **kw):
+    """Allocating form of csa_rope: (x rotated, y rotated or None)."""
+    out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    y_out = None if y is None else torch.empty(y.shape, dtype=y.dtype, device=y.device)
+    csa_rope(x, out, freqs, y=y, y_out=y_out, pos=pos, **kw)
+    return out, y_out
+
+
+def hca_attn_prefix(q, kv_p, kv_c, m: int, kv_raw, window: int, with_lse: bool = False, **kw):
+    out = torch.empty_like(q)
+    lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device) if with_lse else None
+    hca_dense_attn_prefix(q, kv_p, kv_c, m, kv_raw, window, out, lse_out=lse, **kw)
+    return (out, lse) if with_lse else out
+
+
+def entry_weights(q, kv_c, m: int, lse, weight=None, **kw) -> torch.Tensor:
+    """Allocating form of hca_entry_weights: weight (or 0) + what each entry received."""
+    out = torch.empty(kv_c.shape[:2], dtype=torch.float32, device=kv_c.device)
+    hca_entry_weights(q, kv_c, m, lse, out, weight_in=weight, **kw)
+    return out
+
+
+def evict(weight, budget: int, recent: int = 0, n_entries=None, stream=None):
+    """Allocating form of csa_evict: (idx, n_kept); weight is updated in place."""
+    idx = torch.empty(weight.shape[0], budget, dtype=torch.int32, device=weight.device)
+    n_kept = torch.empty(weight.shape[0], dtype=torch.int32, device=weight.device)
+    csa_evict(weight, budget, idx, n_kept, recent=recent, n_entries=n_entries, stream=stream)
+    return idx, n_kept
 
 
 def csa_prefill(q, kv, qI, kI_raw, W_c, W_Ic, m: int, topk: int, window: int,

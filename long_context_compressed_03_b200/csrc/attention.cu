@@ -66,8 +66,10 @@ __global__ void __launch_bounds__(kThreads) attn_generic_kernel(AttnArgs a) {
             const int kk = base + threadIdx.x;
             const T* ptr = nullptr;
             if (kk < rk.n_comp) {
-                const int s = a.dense ? kk : a.idx[(size_t)row * a.topk + kk];
-                if (s >= 0 && s < a.N_cap) {
+                const int s = (a.dense ? kk : a.idx[(size_t)row * a.topk + kk]) - a.N_p;
+                if (s < 0 && a.N_p > 0) {                  // an entry of the shared prefix
+                    ptr = static_cast<const T*>(a.kv_p) + (size_t)kk * D;
+                } else if (s >= 0 && s < a.N_cap) {
                     const long r = cache_row(a.pages, a.N_cap, b, s);
                     if (r >= 0) ptr = kvc + (size_t)r * D;
                 }
@@ -172,6 +174,13 @@ cudaError_t launch_attention_packed(const AttnArgs& a, cudaStream_t s) {
     uint32_t* err = device_error_word();
     if (!err) return cudaErrorUnknown;
     return launch_attention_tc(a, err, s);
+}
+
+unsigned long long attention_prefix_workspace(const AttnArgs&) { return 0; }
+
+cudaError_t launch_attention_prefix(const AttnArgs& a, void*, cudaStream_t s, const char** why) {
+    if (a.dt == DT_F32) return launch_dims<float>(a, s, why);
+    return launch_dims<__nv_bfloat16>(a, s, why);
 }
 
 cudaError_t launch_attention(const AttnArgs& a, cudaStream_t s, const char** why) {

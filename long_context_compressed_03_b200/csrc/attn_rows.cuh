@@ -20,7 +20,8 @@ struct RowKeys {
 __device__ __forceinline__ RowKeys row_keys(const AttnArgs& a, int b, int t) {
     RowKeys k;
     if (a.dense) {
-        const int ne = clampi(a.n_entries ? a.n_entries[b] : a.N_cap, 0, a.N_cap);
+        const int cap = a.N_p + a.N_cap;
+        const int ne = clampi(a.n_entries ? a.n_entries[b] : cap, 0, cap);
         k.n_comp = t < 0 ? 0 : min((t + 1) / a.m, ne);
     } else {
         k.n_comp = a.topk;

@@ -351,14 +351,16 @@ csa_status_t csa_indexer_topk_paged(const void* qI, int qI_dt, const float* qI_s
                         H_I, d_I, N_cap, n_entries, q_pos, m, topk, idx_out, pm, stream);
 }
 
-static csa_status_t attention_common(const char* name, csa::AttnArgs& a, void* stream) {
+// Validates an attention call and fills in the default scale; *empty: it has no query rows.
+static csa_status_t attention_checks(const char* name, csa::AttnArgs& a, bool* empty) {
     REQUIRE(a.B >= 0 && a.n_q >= 0 && a.N_cap >= 0 && a.L_raw >= 0, "%s: negative size", name);
     REQUIRE(a.H >= 1 && a.D >= 1, "%s: H and D must be positive", name);
     REQUIRE(a.window >= 0, "%s: window must be >= 0", name);
     REQUIRE(is_dt(a.dt), "%s: unknown dtype", name);
     if (is_fp8(a.dt)) return fail(CSA_ERR_UNSUPPORTED, "%s: dt must be F32 or BF16", name);
     if (a.D % 16 || a.D > 256) return fail(CSA_ERR_UNSUPPORTED, "%s: D must be a multiple of 16 <= 256", name);
-    if ((long)a.B * a.n_q == 0) return ok();
+    *empty = (long)a.B * a.n_q == 0;
+    if (*empty) return ok();
     REQUIRE(a.q && a.out, "%s: null q or out", name);
     REQUIRE(a.kv_c || a.N_cap == 0, "%s: null kv_c", name);
     REQUIRE(a.kv_raw || a.L_raw == 0, "%s: null kv_raw", name);
@@ -373,6 +375,13 @@ static csa_status_t attention_common(const char* name, csa::AttnArgs& a, void* s
     REQUIRE_ALIGNED4(a.q_pos, "q_pos");
     REQUIRE_ALIGNED4(a.n_entries, "n_entries");
     if (!(a.scale > 0.0f)) a.scale = 1.0f / sqrtf((float)a.D);
+    return ok();
+}
+
+static csa_status_t attention_common(const char* name, csa::AttnArgs& a, void* stream) {
+    bool empty = false;
+    const csa_status_t st = attention_checks(name, a, &empty);
+    if (st != CSA_OK || empty) return st;
     const char* why = nullptr;
     return from_cuda(LAUNCH(csa::launch_attention(a, static_cast<cudaStream_t>(stream), &why)), name, why);
 }
@@ -473,6 +482,216 @@ csa_status_t hca_dense_attn_at(const void* q, int dt, int B, int n_q, int H, int
     a.pos0 = q_pos0;
     a.raw_base = raw_pos0;
     return attention_common("hca_dense_attn_at", a, stream);
+}
+
+// ------------------------------------------------------------ shared prefix
+unsigned long long hca_dense_attn_prefix_workspace(int dt, int B, int n_q, int H, int D, int N_p,
+                                                   int N_cap, int window) {
+    if (B <= 0 || n_q <= 0 || H <= 0 || N_p < 0 || N_cap < 0 || window < 0) return 0;
+    csa::AttnArgs a{};
+    a.dt = dt;
+    a.B = B;
+    a.n_q = n_q;
+    a.H = H;
+    a.D = D;
+    a.N_cap = N_cap;
+    a.dense = 1;
+    a.m = 1;
+    a.window = window;
+    a.N_p = N_p;
+    return csa::attention_prefix_workspace(a);
+}
+
+csa_status_t hca_dense_attn_prefix(const void* q, int dt, int B, int n_q, int H, int D,
+                                   const void* kv_p, int N_p, const void* kv_c, int N_cap,
+                                   const int* n_entries, int m, const void* kv_raw, int L_raw,
+                                   const int* raw_pos0, const int* raw_len, int window,
+                                   const int* q_pos, float softmax_scale, void* out,
+                                   float* lse_out, void* workspace,
+                                   unsigned long long workspace_bytes, void* stream) {
+    const char* name = "hca_dense_attn_prefix";
+    REQUIRE(m >= 1, "%s: m must be >= 1", name);
+    REQUIRE(N_p >= 0 && N_cap >= 0, "%s: negative N_p or N_cap", name);
+    REQUIRE((long)N_p + N_cap <= (1L << 30), "%s: N_p + N_cap above 2^30", name);
+    REQUIRE(kv_p || N_p == 0 || (long)B * n_q == 0, "%s: null kv_p", name);
+    REQUIRE_ALIGNED(kv_p, "kv_p");
+    csa::AttnArgs a{q, dt, B, n_q, H, D, kv_c, N_cap, nullptr, 0, n_entries, m, 1, kv_raw, L_raw,
+                    raw_pos0, raw_len, window, q_pos, softmax_scale, out, lse_out};
+    a.kv_p = kv_p;
+    a.N_p = N_p;
+    bool empty = false;
+    const csa_status_t st = attention_checks(name, a, &empty);
+    if (st != CSA_OK || empty) return st;
+    const unsigned long long need = csa::attention_prefix_workspace(a);
+    REQUIRE(need == 0 || (workspace && workspace_bytes >= need),
+            "%s: the workspace has %llu bytes, %llu are needed", name,
+            workspace ? workspace_bytes : 0ull, need);
+    REQUIRE_ALIGNED(workspace, "workspace");
+    const char* why = nullptr;
+    const cudaError_t e = LAUNCH(csa::launch_attention_prefix(a, workspace, static_cast<cudaStream_t>(stream), &why));
+    return from_cuda(e, name, why);
+}
+
+// ------------------------------------------------------------ entry weights and eviction
+csa_status_t hca_entry_weights(const void* q, int dt, int B, int n_q, int H, int D,
+                               const void* kv_c, int N_cap, const int* idx, int topk,
+                               const int* n_entries, int m, const int* q_pos,
+                               float softmax_scale, const float* lse, const float* weight_in,
+                               float* weight_out, void* stream) {
+    const char* name = "hca_entry_weights";
+    REQUIRE(B >= 0 && n_q >= 0 && N_cap >= 0 && topk >= 0, "%s: negative size", name);
+    REQUIRE(H >= 1 && D >= 1, "%s: H and D must be positive", name);
+    REQUIRE(m >= 1, "%s: m must be >= 1", name);
+    REQUIRE(is_dt(dt), "%s: unknown dtype", name);
+    REQUIRE(idx || topk == 0, "%s: null idx", name);
+    if (is_fp8(dt)) return fail(CSA_ERR_UNSUPPORTED, "%s: dt must be F32 or BF16", name);
+    if (D % 16 || D > 256) return fail(CSA_ERR_UNSUPPORTED, "%s: D must be a multiple of 16 <= 256", name);
+    if ((long)B * std::max(N_cap, topk) > (1L << 31) - 1)
+        return fail(CSA_ERR_UNSUPPORTED, "%s: more than 2^31 - 1 entries or slots", name);
+    if ((long)n_q * H > (1L << 30)) return fail(CSA_ERR_UNSUPPORTED, "%s: n_q * H above 2^30", name);
+    if ((long)B * N_cap == 0) return ok();
+    REQUIRE(weight_out, "%s: null weight_out", name);
+    REQUIRE(n_q == 0 || (q && lse), "%s: null q or lse", name);
+    REQUIRE(kv_c, "%s: null kv_c", name);
+    REQUIRE_ALIGNED(q, "q");
+    REQUIRE_ALIGNED(kv_c, "kv_c");
+    REQUIRE_ALIGNED4(idx, "idx");
+    REQUIRE_ALIGNED4(n_entries, "n_entries");
+    REQUIRE_ALIGNED4(q_pos, "q_pos");
+    REQUIRE_ALIGNED4(lse, "lse");
+    REQUIRE_ALIGNED4(weight_in, "weight_in");
+    REQUIRE_ALIGNED4(weight_out, "weight_out");
+    if (!(softmax_scale > 0.0f)) softmax_scale = 1.0f / sqrtf((float)D);
+    csa::WeightsArgs a{q, dt, B, n_q, H, D, kv_c, N_cap, idx, topk, n_entries, m, q_pos,
+                       softmax_scale, lse, weight_in, weight_out};
+    return from_cuda(LAUNCH(csa::launch_entry_weights(a, static_cast<cudaStream_t>(stream))), name, nullptr);
+}
+
+csa_status_t csa_evict(float* weight, int B, int N_cap, const int* n_entries, int budget,
+                       int recent, int* idx_out, int* n_kept, void* stream) {
+    const char* name = "csa_evict";
+    REQUIRE(B >= 0 && N_cap >= 0, "%s: negative B or N_cap", name);
+    REQUIRE(budget >= 0 && recent >= 0, "%s: negative budget or recent", name);
+    if (N_cap > (1 << 30)) return fail(CSA_ERR_UNSUPPORTED, "%s: N_cap above 2^30", name);
+    if (B == 0) return ok();
+    REQUIRE(weight || N_cap == 0, "%s: null weight", name);
+    REQUIRE(idx_out || budget == 0, "%s: null idx_out", name);
+    REQUIRE_ALIGNED4(weight, "weight");
+    REQUIRE_ALIGNED4(n_entries, "n_entries");
+    REQUIRE_ALIGNED4(idx_out, "idx_out");
+    REQUIRE_ALIGNED4(n_kept, "n_kept");
+    csa::EvictArgs a{weight, B, N_cap, n_entries, budget, std::min(recent, N_cap), idx_out, n_kept};
+    return from_cuda(LAUNCH(csa::launch_evict(a, static_cast<cudaStream_t>(stream))), name, nullptr);
+}
+
+// ------------------------------------------------------------ rotary positions
+csa_status_t csa_rope_freqs(int d_rot, double base, double factor, int original_len,
+                            double beta_fast, double beta_slow, double* freqs, float* scale) {
+    const char* name = "csa_rope_freqs";
+    REQUIRE(d_rot >= 2 && d_rot % 2 == 0, "%s: d_rot must be even and >= 2", name);
+    REQUIRE(base > 1.0 && std::isfinite(base), "%s: base must be > 1", name);
+    REQUIRE(factor >= 1.0 && std::isfinite(factor), "%s: factor must be >= 1", name);
+    REQUIRE(factor == 1.0 || (original_len >= 1 && beta_slow > 0.0 && beta_fast > beta_slow &&
+                              std::isfinite(beta_fast)),
+            "%s: scaling needs original_len >= 1 and beta_fast > beta_slow > 0", name);
+    REQUIRE(freqs, "%s: null freqs", name);
+    const int half = d_rot / 2;
+    const double two_pi = 6.283185307179586476925286766559;
+    // the (real-valued) pair that makes `turns` turns within original_len positions
+    const auto pair_of = [&](double turns) {
+        return d_rot * std::log(original_len / (turns * two_pi)) / (2.0 * std::log(base));
+    };
+    double lo = 0.0, hi = 0.0;
+    if (factor > 1.0) {
+        lo = std::max(std::floor(pair_of(beta_fast)), 0.0);
+        hi = std::min(std::ceil(pair_of(beta_slow)), (double)(d_rot - 1));
+        if (!(hi > lo)) hi = lo + 0.001;
+    }
+    for (int j = 0; j < half; ++j) {
+        const double f = std::pow(base, -2.0 * j / d_rot);
+        if (factor > 1.0) {
+            const double ramp = std::min(std::max((j - lo) / (hi - lo), 0.0), 1.0);
+            freqs[j] = f / factor * ramp + f * (1.0 - ramp);
+        } else {
+            freqs[j] = f;
+        }
+    }
+    if (scale) *scale = factor > 1.0 ? (float)(0.1 * std::log(factor) + 1.0) : 1.0f;
+    return ok();
+}
+
+csa_status_t csa_rope(const void* x, void* x_out, int H, const long long* x_strides,
+                      const void* y, void* y_out, int H_y, const long long* y_strides, int dt,
+                      int B, int n, int D, int d_rot, int rot_offset, int interleaved,
+                      const double* freqs, float scale, const int* pos, int pos0, int pos_step,
+                      int transpose, void* stream) {
+    const char* name = "csa_rope";
+    REQUIRE(B >= 0 && n >= 0 && H >= 0 && H_y >= 0, "%s: negative size", name);
+    REQUIRE(dt == CSA_DT_F32 || dt == CSA_DT_BF16, "%s: dt must be F32 or BF16", name);
+    REQUIRE(D >= 1, "%s: D must be positive", name);
+    REQUIRE(d_rot >= 2 && d_rot % 2 == 0, "%s: d_rot must be even and >= 2", name);
+    REQUIRE(rot_offset >= 0 && (long)rot_offset + d_rot <= D, "%s: the rotated part must lie in the head", name);
+    REQUIRE((interleaved == 0 || interleaved == 1) && (transpose == 0 || transpose == 1),
+            "%s: interleaved and transpose must be 0 or 1", name);
+    REQUIRE(pos || pos0 >= 0, "%s: pos0 must be >= 0", name);
+    REQUIRE(pos || pos_step >= 0, "%s: pos_step must be >= 0", name);
+    REQUIRE(std::isfinite(scale), "%s: scale must be finite", name);
+    REQUIRE(freqs, "%s: null freqs", name);
+    if (d_rot > 2 * csa::kMaxRopePairs)
+        return fail(CSA_ERR_UNSUPPORTED, "%s: d_rot above %d", name, 2 * csa::kMaxRopePairs);
+    if (D > 4096 || H > 4096 || H_y > 4096)
+        return fail(CSA_ERR_UNSUPPORTED, "%s: D, H and H_y above 4096", name);
+    if ((long)B * n > (1L << 31) - 1) return fail(CSA_ERR_UNSUPPORTED, "%s: more than 2^31 - 1 tokens", name);
+    csa::RopeArgs a{};
+    const void* const xs[2] = {x, y};
+    void* const os[2] = {x_out, y_out};
+    const int hs[2] = {H, H_y};
+    const long long* const st[2] = {x_strides, y_strides};
+    for (int w = 0; w < 2; ++w) {
+        const char* which = w ? "y" : "x";
+        a.x[w] = xs[w];
+        a.out[w] = os[w];
+        a.H[w] = hs[w];
+        const long dense[4] = {(long)hs[w] * D, D, (long)hs[w] * D, D};
+        for (int i = 0; i < 4; ++i) {
+            const long v = st[w] ? (long)st[w][i] : dense[i];
+            (i < 2 ? a.xs[w] : a.os[w])[i & 1] = v;
+            REQUIRE(v >= 0 && v <= (1L << 40), "%s: a stride of %s is negative or above 2^40", name, which);
+        }
+        if (hs[w] == 0 || (long)B * n == 0) continue;
+        REQUIRE(xs[w] && os[w], "%s: null %s", name, which);
+        REQUIRE(hs[w] == 1 || a.os[w][1] >= D, "%s: the output heads of %s overlap", name, which);
+        REQUIRE((long)B * n == 1 || a.os[w][0] >= (hs[w] - 1) * a.os[w][1] + D,
+                "%s: the output tokens of %s overlap", name, which);
+        REQUIRE(xs[w] != os[w] || (a.xs[w][0] == a.os[w][0] && a.xs[w][1] == a.os[w][1]),
+                "%s: in place, %s and its output need the same strides", name, which);
+        REQUIRE_ALIGNED(xs[w], which);
+        REQUIRE_ALIGNED(os[w], which);
+    }
+    REQUIRE_ALIGNED4(pos, "pos");
+    if ((long)B * n * (H + H_y) == 0) return ok();
+    // frequencies as 64-bit fractions of a turn (whole turns drop out)
+    const long double inv_two_pi = 0.159154943091895335768883763372514362L;
+    for (int j = 0; j < d_rot / 2; ++j) {
+        REQUIRE(std::isfinite(freqs[j]) && std::fabs(freqs[j]) <= 1e6, "%s: freqs[%d] is not finite or above 10^6", name, j);
+        long double turn = (long double)freqs[j] * inv_two_pi;
+        turn -= floorl(turn);
+        const long double f = turn * 18446744073709551616.0L;
+        a.turn[j] = f >= 18446744073709551615.0L ? 0ull : (uint64_t)(f + 0.5L);
+    }
+    a.dt = dt;
+    a.B = B;
+    a.n = n;
+    a.D = D;
+    a.d_rot = d_rot;
+    a.off = rot_offset;
+    a.interleaved = interleaved;
+    a.transpose = transpose;
+    a.pos = pos;
+    a.pos0 = pos0;
+    a.pos_step = pos_step;
+    a.scale = scale;
+    return from_cuda(LAUNCH(csa::launch_rope(a, static_cast<cudaStream_t>(stream))), name, nullptr);
 }
 
 // ------------------------------------------------------------------ test hooks

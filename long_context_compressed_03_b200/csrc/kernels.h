@@ -109,6 +109,48 @@ struct AttnArgs {
                                      // tokens, N_cap = total entries
     int pos0 = 0;              // q_pos == NULL: query q of every element sits at pos0 + q
     int raw_base = 0;          // raw_pos0 == NULL: raw row j of every element holds position raw_base + j
+    // Shared prefix (dense mode): logical entries 0 .. N_p - 1 of every element
+    // are the rows of kv_p, entry N_p + s of element b is kv_c row (b, s).
+    const void* kv_p = nullptr;
+    int N_p = 0;
+};
+
+// Rotary positions of up to two tensors (x[w]: H[w] heads a token).
+constexpr int kMaxRopePairs = 128;
+struct RopeArgs {
+    const void* x[2];
+    void* out[2];
+    int H[2];                  // 0: no such tensor
+    long xs[2][2], os[2][2];   // {token, head} strides in elements
+    int dt;
+    int B, n, D, d_rot, off, interleaved, transpose;
+    const int* pos;            // [B, n], or NULL: pos0 + j * pos_step
+    long pos0;
+    int pos_step;
+    float scale;
+    uint64_t turn[kMaxRopePairs];   // frequencies as fractions of a turn, times 2^64
+};
+
+struct WeightsArgs {
+    const void* q; int dt;
+    int B, n_q, H, D;
+    const void* kv_c; int N_cap;
+    const int* idx; int topk;  // one list of entries per element, or NULL: every visible entry
+    const int* n_entries; int m;
+    const int* q_pos;
+    float scale;
+    const float* lse;
+    const float* in;           // [B, N_cap] or NULL (zeros); may be out
+    float* out;
+};
+
+struct EvictArgs {
+    float* weight;
+    int B, N_cap;
+    const int* n_entries;
+    int budget, recent;
+    int* idx_out;
+    int* n_kept;
 };
 
 // Device address of this library's error word on the current device (set by
@@ -166,5 +208,13 @@ cudaError_t launch_compress_gated(const GatedArgs& a, cudaStream_t s, const char
 cudaError_t launch_compress_append(const AppendArgs& a, cudaStream_t s, const char** why);
 cudaError_t launch_indexer_topk(const IndexerArgs& a, cudaStream_t s, const char** why);
 cudaError_t launch_attention(const AttnArgs& a, cudaStream_t s, const char** why);
+// Attention over a shared prefix (a.kv_p, a.N_p); the workspace it needs for a
+// call of these sizes, in bytes (0: none).
+unsigned long long attention_prefix_workspace(const AttnArgs& a);
+cudaError_t launch_attention_prefix(const AttnArgs& a, void* workspace, cudaStream_t s,
+                                    const char** why);
+cudaError_t launch_rope(const RopeArgs& a, cudaStream_t s);
+cudaError_t launch_entry_weights(const WeightsArgs& a, cudaStream_t s);
+cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s);
 
 }  // namespace csa

@@ -1,0 +1,422 @@
+"""Rotary positions, shared-prefix attention, entry weights and eviction on the
+GPU, against their definitions in 64 bits (longctx_ref)."""
+import math
+
+import pytest
+import torch
+
+import longctx_ref as ref
+from long_context_compressed_03_b200 import api
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def gen(seed):
+    return torch.Generator(device=DEV).manual_seed(seed)
+
+
+def normal(g, dt, *shape):
+    return torch.randn(*shape, generator=g, device=DEV).to(dt)
+
+
+def i32(v):
+    return torch.tensor(v, dtype=torch.int32, device=DEV)
+
+
+def within(got, want, bound, what):
+    got = got.double()
+    assert torch.equal(torch.isfinite(got), torch.isfinite(want)), f"{what}: infinities or NaN differ"
+    fin = torch.isfinite(want)
+    bad = ((got - want).abs() > bound)[fin]
+    assert not bool(bad.any()), (what, int(bad.sum()), float(((got - want).abs() - bound)[fin].max()))
+
+
+# ------------------------------------------------------------------ rotary positions
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("interleaved", [True, False])
+@pytest.mark.parametrize("B,n,H,Hy,D,rot,off", [
+    (1, 1, 1, 0, 16, 2, 0), (3, 1, 64, 1, 128, 64, 64), (2, 37, 5, 2, 64, 64, 0), (1, 200, 1, 1, 128, 32, 96),
+    (2, 9, 3, 1, 80, 50, 30), (1, 5, 2, 0, 33, 14, 3), (5, 3, 16, 1, 256, 256, 0), (1, 1000, 1, 0, 64, 16, 8)])
+def test_rope(dt, interleaved, B, n, H, Hy, D, rot, off):
+    g = gen(B * 1000 + n + D)
+    x, y = normal(g, dt, B, n, H, D), normal(g, dt, B, n, Hy, D) if Hy else None
+    pos = torch.randint(0, 1 << 20, (B, n), generator=g, device=DEV, dtype=torch.int32)
+    pos[0, 0] = 0
+    pos[-1, -1] = (1 << 31) - 1
+    if n > 2:
+        pos[-1, n // 2] = -1
+    freqs, scale = api.rope_freqs(rot, factor=16.0, original_len=65536)
+    for transpose in (False, True):
+        out = api.rope(x, freqs, pos=pos, y=y, rot_offset=off, interleaved=interleaved, scale=scale,
+                       transpose=transpose)
+        for v, o in zip((x, y), out):
+            if v is None:
+                assert o is None
+                continue
+            want, bound = ref.rope(v, pos, freqs, off, interleaved, scale, transpose)
+            within(o, want, bound, "rope")
+        xi, yi = x.clone(), None if y is None else y.clone()
+        api.csa_rope(xi, xi, freqs, y=yi, y_out=yi, pos=pos, rot_offset=off, interleaved=interleaved,
+                     scale=scale, transpose=transpose)
+        assert torch.equal(xi, out[0]) and (y is None or torch.equal(yi, out[1]))
+
+
+@pytest.mark.parametrize("dt,D,extra", [(BF, 128, 1), (F32, 64, 3), (BF, 24, 1)])
+def test_rope_strided_views_and_default_positions(dt, D, extra):
+    g, B, n, H = gen(3), 2, 17, 6
+    fused = normal(g, dt, B, n, H + extra, D)
+    x = fused[:, :, :H]
+    freqs, _ = api.rope_freqs(D // 2)
+    pos = (5 + 4 * torch.arange(n, device=DEV, dtype=torch.int32)).expand(B, n)
+    want, bound = ref.rope(x, pos, freqs, 0, False, 1.0, False)
+    out, _ = api.rope(x, freqs, pos0=5, pos_step=4, interleaved=False)
+    within(out, want, bound, "rope of a view")
+    rest = fused[:, :, H:].clone()
+    api.csa_rope(x, x, freqs, pos0=5, pos_step=4, interleaved=False)          # in place in the view
+    assert torch.equal(x, out) and torch.equal(fused[:, :, H:], rest)
+    void = torch.full((B, n), -1, dtype=torch.int32, device=DEV)
+    v = normal(g, dt, B, n, H, D)
+    v[0, 0, 0, 0] = math.inf
+    v[0, 1, 0, 1] = math.nan
+    same, _ = api.rope(v, freqs, pos=void)
+    assert torch.equal(same.view(torch.uint8), v.view(torch.uint8))           # passed on bit for bit
+
+
+def test_rope_gradient():
+    # the transposed call is the gradient of the rotation: against central differences of
+    # sum(w * rope(x)), which is linear in x, so a difference over any step is exact up to rounding
+    g, B, n, H, D = gen(8), 1, 4, 2, 16
+    x, w = normal(g, F32, B, n, H, D), normal(g, F32, B, n, H, D)
+    pos = i32([[3, 70000, 12, 999999]])
+    freqs, scale = api.rope_freqs(8, factor=4.0, original_len=4096)
+    kw = dict(pos=pos, rot_offset=4, scale=scale)
+    grad, _ = api.rope(w, freqs, transpose=True, **kw)
+    for k in range(0, x.numel(), 7):
+        e = torch.zeros_like(x)
+        e.view(-1)[k] = 1.0
+        hi, lo = api.rope(x + e, freqs, **kw)[0].double(), api.rope(x - e, freqs, **kw)[0].double()
+        diff = float((w.double() * (hi - lo)).sum()) / 2
+        # each of the four rotated values carries 4.6e-7 of |a| + |b| (<= 12 here) and of scale
+        # (1.14), times |w| <= 4, and x +- 1 rounds once
+        assert abs(diff - float(grad.view(-1)[k])) <= 4 * 4 * (4.6e-7 * 12 * 1.14 + 2.0 ** -22)
+    back, _ = api.rope(api.rope(x, freqs, pos=pos)[0], freqs, pos=pos, transpose=True)
+    assert float((back - x).abs().max()) <= 2 * 2 * 4.6e-7 * 12           # scale 1: the inverse
+
+
+# ------------------------------------------------------------------ shared prefix
+def prefix_case(seed, dt, B, nq, H, D, Np, cap, W, m=4, L=None, void=()):
+    g = gen(seed)
+    L = W + nq - 1 if L is None else L
+    own = torch.randint(0, cap + 1, (B,), generator=g, device=DEV, dtype=torch.int32)
+    last = (Np + own) * m + torch.randint(0, m, (B,), generator=g, device=DEV, dtype=torch.int32) - 1 + nq * m
+    pos = last[:, None] - (nq - 1) + torch.arange(nq, device=DEV, dtype=torch.int32)
+    for b in void:
+        pos[b] = -1
+    return dict(q=normal(g, dt, B, nq, H, D), kv_p=normal(g, dt, Np, D), kv_c=normal(g, dt, B, cap, D), m=m,
+                kv_raw=normal(g, dt, B, L, D), window=W, n_entries=(Np + own).contiguous(),
+                raw_pos0=(last - (L - 1)).contiguous(), raw_len=i32([L] * B), q_pos=pos.contiguous())
+
+
+def run_prefix(a, **kw):
+    a = dict(a)
+    return api.hca_attn_prefix(a.pop("q"), a.pop("kv_p"), a.pop("kv_c"), a.pop("m"), a.pop("kv_raw"),
+                               a.pop("window"), with_lse=True, **a, **kw)
+
+
+def check_prefix(a, dt, **kw):
+    out, lse = run_prefix(a, **kw)
+    want, wl, bound, bl = ref.prefix_attention(dict(a, scale=kw.get("softmax_scale")), dt, BF if dt == BF else None)
+    within(out, want, bound, "prefix attention")
+    within(lse, wl, bl, "prefix attention lse")
+    return out, lse
+
+
+@pytest.mark.parametrize("dt,B,nq,H,D,Np,cap,W", [
+    (BF, 1, 1, 64, 128, 1, 0, 0), (BF, 1, 1, 64, 128, 128, 0, 1), (BF, 3, 1, 64, 128, 129, 3, 16),
+    (BF, 2, 2, 64, 128, 700, 70, 65), (BF, 5, 3, 64, 128, 383, 200, 130), (BF, 4, 1, 128, 128, 260, 9, 40),
+    (BF, 3, 2, 128, 128, 511, 129, 128), (BF, 9, 1, 64, 128, 1000, 1, 300), (BF, 3, 1, 16, 64, 90, 10, 20),
+    (BF, 3, 1, 32, 128, 300, 10, 20), (BF, 2, 1, 64, 128, 0, 40, 20), (BF, 2, 2, 64, 128, 0, 0, 33),
+    (F32, 2, 3, 8, 64, 300, 20, 32), (F32, 1, 1, 8, 64, 1, 0, 0), (F32, 3, 1, 16, 128, 77, 5, 9),
+    (F32, 2, 1, 64, 128, 130, 5, 9), (F32, 5, 1, 8, 64, 1000, 40, 100)])
+def test_prefix_attention(dt, B, nq, H, D, Np, cap, W):
+    check_prefix(prefix_case(B * 100 + Np, dt, B, nq, H, D, Np, cap, W), dt)
+
+
+@pytest.mark.parametrize("dt,H,D", [(BF, 64, 128), (BF, 128, 128), (F32, 8, 64)])
+def test_prefix_partial_visibility_empty_rows_and_poison(dt, H, D):
+    # rows that see no key, only part of the prefix, no window, a cache slot before position 0;
+    # whatever a row may not see is NaN or infinite
+    B, nq, Np, cap, W, m, L = 7, 2, 300, 50, 24, 4, 40
+    a = prefix_case(5, dt, B, nq, H, D, Np, cap, W, m=m, L=L)
+    a["n_entries"] = i32([0, 10, 130, 299, 300, 301, 345])
+    a["q_pos"] = i32([[-1, 2], [5, 4000], [-1, -1], [1100, 1201], [5000, 5001], [1203, 1204], [9000, 9001]])
+    a["raw_pos0"] = i32([-30, -8, 0, 1170, 4970, 1180, 8000])
+    a["raw_len"] = i32([40, 20, 0, 40, 32, 25, 40])
+    vis = torch.minimum((a["q_pos"] + 1) // m, a["n_entries"][:, None]).amax(1)
+    for b in range(B):
+        own = max(int(vis[b]) - Np, 0)
+        a["kv_c"][b, own:] = math.nan if b % 2 else math.inf
+        for i in range(L):
+            p = int(a["raw_pos0"][b]) + i
+            if i >= int(a["raw_len"][b]) or p < 0 or p > int(a["q_pos"][b].max()):
+                a["kv_raw"][b, i] = -math.inf if b % 2 else math.nan
+    out, lse = check_prefix(a, dt)
+    assert bool((out[2] == 0).all()) and bool((lse[2] == -math.inf).all())
+    # a prefix poisoned past what a group of elements sees leaves those elements finite
+    a["kv_p"][130:] = math.nan
+    out, lse = run_prefix(a)
+    want, wl, bound, bl = ref.prefix_attention(a, dt, BF if dt == BF else None)
+    for b in range(3):
+        within(out[b], want[b], bound[b], "below the poison")
+        within(lse[b], wl[b], bl[b], "below the poison")
+    a["n_entries"] = a["n_entries"].clamp(max=130)
+    a["kv_c"][:] = math.nan
+    check_prefix(a, dt)
+
+
+@pytest.mark.parametrize("H", [64, 128])
+def test_prefix_defaults_scale_and_large_scores(H):
+    # no optional arrays (positions 0 .. n_q - 1: a prefill over a prefix of m = 1 entries), a given
+    # scale, keys of magnitude ~50 (one weight close to 1)
+    g = gen(11)
+    a = dict(q=normal(g, BF, 2, 130, H, 128), kv_p=normal(g, BF, 70, 128) * 4, kv_c=normal(g, BF, 2, 30, 128),
+             m=1, kv_raw=normal(g, BF, 2, 130, 128), window=20, n_entries=None, raw_pos0=None, raw_len=None,
+             q_pos=None)
+    check_prefix(a, BF, softmax_scale=0.5)
+
+
+def test_prefix_matches_dense_call_on_the_whole_cache():
+    a = prefix_case(21, BF, 6, 1, 64, 128, 900, 60, 128, m=128)
+    out, lse = run_prefix(a)
+    whole = torch.cat([a["kv_p"].expand(6, -1, -1), a["kv_c"]], 1).contiguous()
+    o2, l2 = api.hca_attn(a["q"], whole, 128, a["kv_raw"], 128, with_lse=True, n_entries=a["n_entries"],
+                          raw_pos0=a["raw_pos0"], raw_len=a["raw_len"], q_pos=a["q_pos"])
+    want, wl, bound, bl = ref.prefix_attention(a, BF, BF)
+    assert bool(((out.double() - o2.double()).abs() <= 2 * bound).all())
+    assert bool(((lse.double() - l2.double()).abs() <= 2 * bl).all())
+
+
+def test_prefix_is_deterministic_and_leaves_its_inputs():
+    a = prefix_case(31, BF, 33, 1, 64, 128, 1500, 40, 200, m=128)
+    before = {k: v.clone() for k, v in a.items() if isinstance(v, torch.Tensor)}
+    o1, l1 = run_prefix(a)
+    for _ in range(3):
+        o2, l2 = run_prefix(a)
+        assert torch.equal(o1, o2) and torch.equal(l1, l2)
+    assert all(torch.equal(a[k], v) for k, v in before.items())
+
+
+# ------------------------------------------------------------------ entry weights
+def weights_case(seed, dt, B, nq, H, D, N, m=4, topk=0):
+    g = gen(seed)
+    q, kv = normal(g, dt, B, nq, H, D), normal(g, dt, B, N, D)
+    ne = torch.randint(N // 2, N + 1, (B,), generator=g, device=DEV, dtype=torch.int32)
+    pos = ((ne * m + m - 2)[:, None] - (nq - 1) + torch.arange(nq, device=DEV, dtype=torch.int32)).contiguous()
+    lse = torch.rand(B, nq, H, generator=g, device=DEV) + math.log(N + 1)
+    idx = None
+    if topk:
+        idx = torch.rand(B, N, generator=g, device=DEV).argsort(1)[:, :topk].to(torch.int32).contiguous()
+    return dict(q=q, kv=kv, m=m, lse=lse, weight=torch.rand(B, N, generator=g, device=DEV), idx=idx, n_entries=ne,
+                q_pos=pos)
+
+
+def run_weights(a, **kw):
+    a = dict(a)
+    return api.entry_weights(a.pop("q"), a.pop("kv"), a.pop("m"), a.pop("lse"), **a, **kw)
+
+
+def check_weights(a):
+    got = run_weights(a)
+    want, bound = ref.entry_weights(a["q"], a["kv"], a["m"], a["lse"], a["weight"], a["idx"], a["n_entries"], a["q_pos"])
+    within(got, want, bound, "entry weights")
+    return got
+
+
+@pytest.mark.parametrize("dt,B,nq,H,D,N,topk", [
+    (BF, 1, 1, 64, 128, 1, 0), (BF, 3, 1, 64, 128, 130, 0), (BF, 2, 1, 128, 128, 700, 0), (BF, 2, 5, 64, 128, 259, 0),
+    (BF, 1, 3, 16, 64, 500, 0), (BF, 2, 1, 8, 128, 77, 0), (BF, 2, 2, 5, 48, 33, 0), (BF, 3, 1, 64, 128, 600, 77),
+    (BF, 1, 33, 64, 128, 1030, 0), (BF, 2, 3, 64, 128, 300, 130), (BF, 1, 70, 2, 128, 140, 0),
+    (F32, 2, 1, 8, 64, 300, 0), (F32, 2, 3, 8, 64, 65, 10), (F32, 1, 1, 64, 256, 40, 0)])
+def test_entry_weights(dt, B, nq, H, D, N, topk):
+    check_weights(weights_case(B * 10 + N, dt, B, nq, H, D, N, topk=topk))
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_entry_weights_masks_lists_and_poison(dt):
+    a = weights_case(3, dt, 5, 3, 8, 64, 200, m=4)
+    a["n_entries"] = i32([0, 1, 100, 250, 200])
+    a["q_pos"] = i32([[500, 501, 502], [2, 3, 4], [-1, 300, -1], [700, 798, 799], [-1, -1, -1]])
+    a["lse"][2, 1, 3] = -math.inf                       # an empty row adds nothing
+    a["lse"][3, 0] = -math.inf
+    for b, seen in enumerate((0, 1, 75, 200, 0)):
+        a["kv"][b, seen:] = math.nan if b % 2 else math.inf
+    got = check_weights(a)
+    assert torch.equal(got[0], a["weight"][0]) and torch.equal(got[4], a["weight"][4])
+    a["weight"] = None
+    check_weights(a)
+    # lists: padding, entries outside the cache or not visible, an entry twice
+    a["weight"] = torch.rand(5, 200, device=DEV)
+    a["idx"] = i32([[0, 5, -1, 7]] * 2 + [[74, 75, 74, -3], [199, 0, 250, 199], [1, 2, 3, 4]])
+    check_weights(a)
+    w = a["weight"].clone()
+    api.hca_entry_weights(a["q"], a["kv"], a["m"], a["lse"], w, weight_in=w, idx=a["idx"], n_entries=a["n_entries"],
+                          q_pos=a["q_pos"])             # in place
+    assert torch.equal(w, run_weights(a))
+
+
+def test_entry_weights_of_an_attention_call_sum_to_its_heads():
+    # with the call's own lse and no window, every head's weights add to one
+    g, B, N, H = gen(13), 3, 900, 64
+    q, kv = normal(g, BF, B, 1, H, 128), normal(g, BF, B, N, 128)
+    pos = i32([[4 * N - 1]] * B)
+    _, lse = api.hca_attn(q, kv, 4, torch.zeros(B, 1, 128, dtype=BF, device=DEV), 0, with_lse=True, q_pos=pos)
+    w = api.entry_weights(q, kv, 4, lse, q_pos=pos)
+    # lse and the scores carry ~1e-5 at most (128 products in fp32), a sum of 900 fp32 terms 900 * 2^-24
+    assert float((w.double().sum(1) - H).abs().max()) <= H * 1e-4
+
+
+# ------------------------------------------------------------------ eviction
+@pytest.mark.parametrize("B,N,budget,recent", [
+    (1, 1, 1, 0), (1, 1, 0, 0), (3, 33, 7, 2), (2, 1000, 999, 10), (2, 1000, 100, 300), (5, 777, 100, 0),
+    (1, 5000, 64, 64), (2, 32768, 2048, 128), (1, 40001, 3001, 1), (3, 2000, 2000, 5), (2, 100, 300, 1000),
+    (9, 4096, 512, 17), (1, 150001, 7000, 333)])
+def test_evict(B, N, budget, recent):
+    g = gen(N + budget)
+    w = torch.rand(B, N, generator=g, device=DEV).log().neg()
+    w = torch.where(torch.rand(B, N, generator=g, device=DEV) < 0.3, (w * 4).round() / 4, w)     # ties
+    w = torch.where(torch.rand(B, N, generator=g, device=DEV) < 0.1, torch.full_like(w, -1), w)
+    ne = torch.randint(0, N + 1, (B,), generator=g, device=DEV, dtype=torch.int32)
+    ne[0] = N
+    for n_entries in (ne, None):
+        ww = w.clone()
+        idx, kept = api.evict(ww, budget, recent=recent, n_entries=n_entries)
+        want = ref.evict(w, n_entries, budget, recent)
+        assert torch.equal(idx.cpu(), want[0]) and torch.equal(kept.cpu(), want[1]) and torch.equal(ww.cpu(), want[2])
+        again = api.evict(ww, budget, recent=recent, n_entries=n_entries)       # nothing more goes
+        assert torch.equal(again[0], idx) and torch.equal(again[1], kept)
+
+
+def test_evict_special_weights():
+    w = torch.tensor([[0.0, -0.0, math.nan, math.inf, 1e-45, -1.0, 5.0, 5.0, math.inf, 0.0],
+                      [-1.0] * 10, [math.nan] * 10, [0.0] * 10, [7.0] * 10], device=DEV)
+    for budget in (0, 1, 2, 3, 4, 5, 6, 8, 10, 12):
+        for recent in (0, 1, 3, 20):
+            ww = w.clone()
+            idx, kept = api.evict(ww, budget, recent=recent)
+            want = ref.evict(w, None, budget, recent)
+            assert torch.equal(idx.cpu(), want[0]) and torch.equal(kept.cpu(), want[1])
+            assert torch.equal(ww.cpu().view(torch.int32), want[2].view(torch.int32))
+    ww = w.clone()
+    idx, _ = api.evict(ww, 3, n_entries=i32([-5, 3, 99, 4, 0]))      # counts outside the cache are clamped
+    want = ref.evict(w, [-5, 3, 99, 4, 0], 3, 0)
+    assert torch.equal(idx.cpu(), want[0])
+
+
+# ------------------------------------------------------------------ together
+def test_a_decode_loop_with_eviction():
+    """Rotate, append to the compressed cache, attend to the kept entries and the window,
+    accumulate the weights, evict -- each step against the definitions."""
+    g, B, H, D, m, cap, W, budget, recent = gen(99), 3, 64, 128, 4, 64, 16, 12, 3
+    W_c = normal(g, BF, D, D) / math.sqrt(D)
+    state = torch.zeros(B, 2, D, device=DEV)
+    cache, ne = torch.zeros(B, cap, D, dtype=BF, device=DEV), torch.zeros(B, dtype=torch.int32, device=DEV)
+    weight, raw = torch.zeros(B, cap, device=DEV), torch.zeros(B, W, D, dtype=BF, device=DEV)
+    freqs, _ = api.rope_freqs(64)
+    for step in range(90):
+        pos = i32([[step]] * B)
+        q, kv = api.rope(normal(g, BF, B, 1, H, D), freqs, pos=pos, y=normal(g, BF, B, 1, 1, D), rot_offset=64)
+        raw = torch.cat([raw[:, 1:], kv[:, :, 0]], 1).contiguous()
+        api.csa_compress_append(kv[:, 0, 0].contiguous(), W_c, m, True, pos[:, 0].contiguous(), state, cache, n_entries=ne)
+        before = weight.clone()
+        idx, kept = api.evict(weight, budget, recent=recent, n_entries=ne)
+        want = ref.evict(before, ne.cpu(), budget, recent)
+        assert torch.equal(idx.cpu(), want[0]) and torch.equal(kept.cpu(), want[1])
+        p0 = i32([step - W + 1] * B)
+        out, lse = api.sparse_attn(q, cache, idx, raw, W, with_lse=True, raw_pos0=p0, raw_len=i32([W] * B), q_pos=pos)
+        new = api.entry_weights(q, cache, m, lse, weight=weight, idx=idx, n_entries=ne, q_pos=pos)
+        if step % 10 == 9:
+            w, bound = ref.entry_weights(q, cache, m, lse, weight, idx, ne, pos)
+            within(new, w, bound, "weights")
+            for b in range(B):
+                keys = torch.cat([cache[b, idx[b][idx[b] >= 0].long()], raw[b, max(0, W - 1 - step):]]).double()
+                o, l, bo, bl = ref.attention_row(q[b, 0].double(), keys, D ** -0.5, BF, BF)
+                within(out[b, 0], o, bo, "attention over the kept entries")
+                within(lse[b, 0], l, bl, "lse over the kept entries")
+                assert float(new[b].clamp(min=0).sum()) <= H * (step + 1) * 1.001
+        back, _ = api.rope(out, freqs, pos=pos, rot_offset=64, transpose=True)      # shared KV: turn the output back
+        assert torch.isfinite(back.float()).all()
+        weight = new
+    assert int((weight >= 0).sum(1).max()) <= cap and int(kept[0]) == budget
+
+
+def test_a_shared_prefix_step_with_weights_of_the_own_entries():
+    """A step over a shared prefix, then the weights of each element's own entries from the
+    call's lse: prefix, own entries and window together give every head one."""
+    a = prefix_case(77, BF, 4, 1, 64, 128, 300, 40, 32, m=4)
+    out, lse = run_prefix(a)
+    B, cap, Np = 4, 40, 300
+    pos_own = (a["q_pos"] - Np * a["m"]).contiguous()          # the own cache counts from the prefix's end
+    own = api.entry_weights(a["q"], a["kv_c"], a["m"], lse, n_entries=(a["n_entries"] - Np).contiguous(), q_pos=pos_own)
+    pre = api.entry_weights(a["q"], a["kv_p"].expand(B, -1, -1).contiguous(), a["m"], lse, q_pos=a["q_pos"])
+    win = api.entry_weights(a["q"], a["kv_raw"], 1, lse, q_pos=i32([[31]] * B))
+    total = own.double().sum(1) + pre.double().sum(1) + win.double().sum(1)
+    assert float((total - 64).abs().max()) <= 64 * 1e-4
+
+
+# ------------------------------------------------------------------ streams and graphs
+def _ops(a, w, weight):
+    out, lse = run_prefix(a)
+    x, _ = api.rope(out, w["freqs"], pos=a["q_pos"], transpose=True)
+    new = api.entry_weights(a["q"], w["kv"], 4, lse, weight=weight, q_pos=a["q_pos"])
+    idx, kept = api.evict(new, 20, recent=3)
+    return out, lse, x, new, idx, kept
+
+
+def test_side_stream_and_captured_graphs():
+    a = prefix_case(41, BF, 5, 1, 64, 128, 700, 33, 100, m=4)
+    w = dict(kv=normal(gen(42), BF, 5, 90, 128), freqs=api.rope_freqs(64)[0])
+    weight = torch.rand(5, 90, device=DEV)
+    want = _ops(a, w, weight)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = _ops(a, w, weight)
+    side.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
+    b = prefix_case(43, BF, 5, 1, 64, 128, 700, 33, 100, m=4)
+    want_b = _ops(b, w, weight)
+    graphs = []
+    for case in (a, b):                       # two graphs, replayed on two streams at once
+        gr = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(gr):
+            res = _ops(case, w, weight)
+        graphs.append((gr, res))
+    s2 = torch.cuda.Stream()
+    for _ in range(5):
+        for _, res in graphs:
+            for r in res:
+                r.zero_()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            graphs[0][0].replay()
+        with torch.cuda.stream(s2):
+            graphs[1][0].replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(graphs[0][1], want))
+        assert all(torch.equal(x, y) for x, y in zip(graphs[1][1], want_b))
+
+
+def test_stream_argument():
+    a = prefix_case(51, BF, 2, 1, 64, 128, 300, 10, 50, m=4)
+    want = run_prefix(a)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    out, lse = torch.empty_like(want[0]), torch.empty_like(want[1])
+    torch.cuda.synchronize()
+    api.hca_dense_attn_prefix(a["q"], a["kv_p"], a["kv_c"], 4, a["kv_raw"], 50, out, lse_out=lse, stream=s,
+                              **{k: a[k] for k in ("n_entries", "raw_pos0", "raw_len", "q_pos")})
+    s.synchronize()
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
