@@ -176,9 +176,16 @@ cudaError_t launch_attention_packed(const AttnArgs& a, cudaStream_t s) {
     return launch_attention_tc(a, err, s);
 }
 
-unsigned long long attention_prefix_workspace(const AttnArgs&) { return 0; }
+unsigned long long attention_prefix_workspace(const AttnArgs& a) {
+    return attention_prefix_tc_supported(a) ? attention_prefix_tc_workspace(a) : 0;
+}
 
-cudaError_t launch_attention_prefix(const AttnArgs& a, void*, cudaStream_t s, const char** why) {
+cudaError_t launch_attention_prefix(const AttnArgs& a, void* workspace, cudaStream_t s, const char** why) {
+    if (attention_prefix_tc_supported(a)) {
+        uint32_t* err = device_error_word();
+        if (!err) return cudaErrorUnknown;
+        return launch_attention_prefix_tc(a, workspace, err, s);
+    }
     if (a.dt == DT_F32) return launch_dims<float>(a, s, why);
     return launch_dims<__nv_bfloat16>(a, s, why);
 }

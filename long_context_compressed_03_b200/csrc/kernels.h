@@ -208,6 +208,12 @@ cudaError_t launch_compress_gated(const GatedArgs& a, cudaStream_t s, const char
 cudaError_t launch_compress_append(const AppendArgs& a, cudaStream_t s, const char** why);
 cudaError_t launch_indexer_topk(const IndexerArgs& a, cudaStream_t s, const char** why);
 cudaError_t launch_attention(const AttnArgs& a, cudaStream_t s, const char** why);
+// tcgen05 attention over a shared prefix: bf16, 64 or 128 heads x 128.
+bool attention_prefix_tc_supported(const AttnArgs& a);
+unsigned long long attention_prefix_tc_workspace(const AttnArgs& a);
+cudaError_t launch_attention_prefix_tc(const AttnArgs& a, void* workspace, uint32_t* err,
+                                       cudaStream_t s);
+
 // Attention over a shared prefix (a.kv_p, a.N_p); the workspace it needs for a
 // call of these sizes, in bytes (0: none).
 unsigned long long attention_prefix_workspace(const AttnArgs& a);
