@@ -78,7 +78,6 @@ struct __align__(8) Ctrl {
     uint32_t tmem_base;
     int abort;
 };
-constexpr size_t kSmem = 1024 + 2 * kTileBytes + kStages * kTileBytes + sizeof(Ctrl);
 
 struct PrefixParams {
     const __nv_bfloat16* kv_p;
@@ -99,87 +98,92 @@ struct PrefixParams {
     int stall;
 };
 
-// What one query row sees.
-struct Row {
-    bool on;                 // it exists and has a position
+// What one query row sees beyond the unit's shared tiles (all in smem, filled
+// once by the CTA's threads).
+struct RowRec {
+    int on;                  // it exists and has a position
     int b;
     int vis;                 // visible logical entries
     int win_lo, n_win;       // raw rows
+    int n_pre, n_own;        // further prefix entries, own entries
+    int pad;
 };
-__device__ __forceinline__ Row row_of(const PrefixParams& p, int row) {
-    Row r;
-    r.on = row < p.R;
-    r.b = 0;
-    r.vis = r.win_lo = r.n_win = 0;
-    if (!r.on) return r;
-    r.b = row / p.a.n_q;
-    const int t = p.a.q_pos ? __ldg(p.a.q_pos + row) : row - r.b * p.a.n_q;
-    r.on = t >= 0;
-    if (!r.on) return r;
-    const RowKeys k = row_keys(p.a, r.b, t);
-    r.vis = k.n_comp;
-    r.win_lo = k.win_lo;
-    r.n_win = k.n_win;
-    return r;
-}
-// Keys of a row beyond the unit's `shared` prefix entries: the rest of the
-// prefix it sees, its own entries, its window.
-struct Own {
-    int n_pre, n_own, n_win;
-    __device__ __forceinline__ int len() const { return n_pre + n_own + n_win; }
-};
-__device__ __forceinline__ Own own_of(const PrefixParams& p, const Row& r, int shared) {
-    Own o{0, 0, 0};
-    if (r.on) {
-        o.n_pre = max(min(r.vis, p.a.N_p) - shared, 0);
-        o.n_own = max(r.vis - p.a.N_p, 0);
-        o.n_win = r.n_win;
-    }
-    return o;
-}
-
-// A unit's tile list: P shared tiles, then the slots' own tiles, alternating
-// while both have some.
+// A unit's tile list: P shared tiles, then the slots' own tiles (T0, T1),
+// alternating while both have some.
 struct Geo {
-    int P;
-    int T[2];                // own tiles
-    bool on[2];              // the slot has a row with a position
-    __device__ __forceinline__ int total() const { return P + T[0] + T[1]; }
-    __device__ __forceinline__ int mask(int i) const {
-        if (i < P) return (on[0] ? 1 : 0) | (on[1] ? 2 : 0);
-        return 1 << own_slot(i);
-    }
+    int P, T0, T1;
+    int on;                  // bit s: slot s has a row with a position
+    __device__ __forceinline__ int total() const { return P + T0 + T1; }
     __device__ __forceinline__ int own_slot(int i) const {
-        const int j = i - P, both = 2 * min(T[0], T[1]);
-        return j < both ? (j & 1) : (T[0] > T[1] ? 0 : 1);
+        const int j = i - P, both = 2 * min(T0, T1);
+        return j < both ? (j & 1) : (T0 > T1 ? 0 : 1);
     }
     __device__ __forceinline__ int own_step(int i) const {
-        const int j = i - P, lo = min(T[0], T[1]);
+        const int j = i - P, lo = min(T0, T1);
         return j < 2 * lo ? (j >> 1) : j - lo;
     }
-};
-template <int G>
-__device__ __forceinline__ Geo geometry(const PrefixParams& p, int u) {
-    Geo g;
-    Row r[2 * G];
-    int lo = p.a.N_p;
-    g.on[0] = g.on[1] = false;
-#pragma unroll
-    for (int i = 0; i < 2 * G; ++i) {
-        r[i] = row_of(p, u * 2 * G + i);
-        if (r[i].on) {
-            lo = min(lo, r[i].vis);
-            g.on[i / G] = true;
+    // bit s: slot s uses tile i
+    __device__ __forceinline__ int mask(int i) const { return i < P ? on : 1 << own_slot(i); }
+    // the first tile of slot s at or after i (hi: none below it)
+    __device__ __forceinline__ int next_of(int s, int i, int hi) const {
+        if (i < P) {
+            if ((on >> s) & 1) return min(i, hi);
+            i = P;
         }
+        const int lo = min(T0, T1), both = P + 2 * lo;
+        if (i < both) {
+            if (((i - P) & 1) != s) ++i;
+            if (i < both) return min(i, hi);
+        }
+        return (s ? T1 : T0) > lo ? min(i, hi) : hi;
     }
-    g.P = (g.on[0] || g.on[1]) ? lo / kBN : 0;
-    g.T[0] = g.T[1] = 0;
+};
+constexpr int kMaxUnits = 32;            // units a CTA meets, at most
+
+// The CTA's units u0 .. u0 + n - 1: a thread per query row, then one per unit.
+template <int G>
+__device__ __forceinline__ void fill_geometry(const PrefixParams& p, int u0, int n, Geo* geo, RowRec* rows) {
+    for (int i = threadIdx.x; i < n * 2 * G; i += kThreads) {
+        const int row = u0 * 2 * G + i;
+        RowRec r{};
+        if (row < p.R) {
+            r.b = row / p.a.n_q;
+            const int t = p.a.q_pos ? __ldg(p.a.q_pos + row) : row - r.b * p.a.n_q;
+            if (t >= 0) {
+                const RowKeys k = row_keys(p.a, r.b, t);
+                r.on = 1;
+                r.vis = k.n_comp;
+                r.win_lo = k.win_lo;
+                r.n_win = k.n_win;
+            }
+        }
+        rows[i] = r;
+    }
+    __syncthreads();
+    for (int k = threadIdx.x; k < n; k += kThreads) {
+        Geo g{0, 0, 0, 0};
+        int lo = p.a.N_p;
 #pragma unroll
-    for (int i = 0; i < 2 * G; ++i) {
-        const int n = own_of(p, r[i], g.P * kBN).len();
-        g.T[i / G] = max(g.T[i / G], (n + kRows / G - 1) / (kRows / G));
+        for (int i = 0; i < 2 * G; ++i) {
+            const RowRec& r = rows[k * 2 * G + i];
+            if (r.on) {
+                lo = min(lo, r.vis);
+                g.on |= 1 << (i / G);
+            }
+        }
+        g.P = g.on ? lo / kBN : 0;
+#pragma unroll
+        for (int i = 0; i < 2 * G; ++i) {
+            RowRec& r = rows[k * 2 * G + i];
+            if (!r.on) continue;
+            r.n_pre = max(min(r.vis, p.a.N_p) - g.P * kBN, 0);
+            r.n_own = max(r.vis - p.a.N_p, 0);
+            const int T = (r.n_pre + r.n_own + r.n_win + kRows / G - 1) / (kRows / G);
+            if (i < G) g.T0 = max(g.T0, T);
+            else g.T1 = max(g.T1, T);
+        }
+        geo[k] = g;
     }
-    return g;
 }
 
 // The part of unit u that CTA c of n takes, as a range of its tile list.
@@ -199,6 +203,19 @@ __device__ __forceinline__ Part part_of(const PrefixParams& p, int c, int n, int
 __device__ __forceinline__ int first_unit(const PrefixParams& p, int c, int n) { return (int)((long)c * p.U / n); }
 __device__ __forceinline__ int end_unit(const PrefixParams& p, int c, int n) {
     return (int)(((long)(c + 1) * p.U + n - 1) / n);
+}
+
+constexpr size_t kSmem = 1024 + 2 * kTileBytes + kStages * kTileBytes + sizeof(Ctrl) +
+                         kMaxUnits * (sizeof(Geo) + 4 * sizeof(RowRec));
+
+// A bounded wait: one try in line, the rest out of line.
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* err,
+                                       uint64_t limit_ns) {
+    return mbar_wait(bar, parity, abort, err, limit_ns);
+}
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* err,
+                                         uint64_t limit_ns) {
+    return mbar_try_wait(bar, parity) || wait_slow(bar, parity, abort, err, limit_ns);
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -233,6 +250,27 @@ __device__ __forceinline__ void cp_async16_or_zero(void* dst, const void* src, b
                  ::"r"(smem_u32(dst)), "l"(src), "r"(on ? 16 : 0) : "memory");
 }
 
+// Largest S of the row's columns [c_lo, c_hi) (c_lo a multiple of 32; uniform in a warp).
+__device__ __noinline__ float row_max(uint32_t s_addr, int c_lo, int c_hi) {
+    float mx0 = -INFINITY, mx1 = -INFINITY;
+#pragma unroll 1
+    for (int c = c_lo; c < c_hi; c += 32) {
+        float sv[32];
+        tmem_ld32(s_addr + c, sv);
+        if (c_hi < c + 32) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+                if (c + e >= c_hi) sv[e] = -INFINITY;
+        }
+#pragma unroll
+        for (int e = 0; e < 32; e += 4) {
+            mx0 = max3(mx0, sv[e], sv[e + 1]);
+            mx1 = max3(mx1, sv[e + 2], sv[e + 3]);
+        }
+    }
+    return fmaxf(mx0, mx1);
+}
+
 // The row maximum grew by more than 2^8: rescale the row's O in TMEM.
 __device__ __noinline__ void rescale_o(uint32_t o_addr, float alpha) {
 #pragma unroll 1
@@ -256,6 +294,8 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     uint8_t* sQ = base;                                  // [2][32 KB]
     uint8_t* sK = sQ + 2 * kTileBytes;                   // [kStages][32 KB]
     Ctrl* ctl = reinterpret_cast<Ctrl*>(sK + kStages * kTileBytes);
+    Geo* geo = reinterpret_cast<Geo*>(ctl + 1);          // [kMaxUnits]
+    RowRec* rows = reinterpret_cast<RowRec*>(geo + kMaxUnits);   // [kMaxUnits][2 G]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     volatile int* abort = &ctl->abort;
     const int c = blockIdx.x, n_cta = gridDim.x;
@@ -284,6 +324,7 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         tmem_alloc(&ctl->tmem_base, 512);
         tmem_relinquish();
     }
+    fill_geometry<G>(p, u0, u1 - u0, geo, rows);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -307,11 +348,11 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             }
         };
         for (int u = u0; u < u1 && ok; ++u) {
-            const Geo g = geometry<G>(p, u);
+            const Geo g = geo[u - u0];
             const Part pt = part_of(p, c, n_cta, u, g.total());
             for (int i = pt.lo; i < pt.hi; ++i, ++L) {
                 const int slot = L % kStages, use = L / kStages;
-                if (use > 0 && !mbar_wait(&ctl->freeb[slot], (use - 1) & 1, abort, p.err, p.wait_ns)) { ok = false; break; }
+                if (use > 0 && !wait_bar(&ctl->freeb[slot], (use - 1) & 1, abort, p.err, p.wait_ns)) { ok = false; break; }
                 if (*abort) { ok = false; break; }
                 uint8_t* dst = sK + slot * kTileBytes;
                 if (i < g.P) {
@@ -328,27 +369,18 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 } else {
                     if (lt == 0) tma_stage &= ~(1u << slot);
                     const int ms = g.own_slot(i), j0 = g.own_step(i) * H;
-                    Row row[G];
-                    Own own[G];
-#pragma unroll
-                    for (int k = 0; k < G; ++k) {
-                        row[k] = row_of(p, (2 * u + ms) * G + k);
-                        own[k] = own_of(p, row[k], g.P * kBN);
-                    }
+                    const RowRec* rec = rows + ((u - u0) * 2 + ms) * G;
 #pragma unroll 2
                     for (int rr = lt >> 4; rr < kBN; rr += kLoadThreads / 16) {
                         const int k = rr / H, j = j0 + rr % H;
-                        const Row rw = (G == 1 || k == 0) ? row[0] : row[G - 1];
-                        const Own ow = (G == 1 || k == 0) ? own[0] : own[G - 1];
-                        const __nv_bfloat16* src = p.kv_raw;
-                        if (j < ow.n_pre) src = p.kv_p + (size_t)(g.P * kBN + j) * kD;
-                        else if (j < ow.n_pre + ow.n_own)
-                            src = p.kv_c + ((size_t)rw.b * p.a.N_cap + (j - ow.n_pre)) * kD;
-                        else if (j < ow.len())
-                            src = p.kv_raw + ((size_t)rw.b * p.a.L_raw + rw.win_lo + (j - ow.n_pre - ow.n_own)) * kD;
-                        else src = reinterpret_cast<const __nv_bfloat16*>(p.out);
+                        const RowRec rw = rec[k];
+                        const __nv_bfloat16* src = p.out;          // any address: nothing is read past the list
+                        const int e1 = rw.n_pre, e2 = e1 + rw.n_own, e3 = e2 + rw.n_win;
+                        if (j < e1) src = p.kv_p + (size_t)(g.P * kBN + j) * kD;
+                        else if (j < e2) src = p.kv_c + ((size_t)rw.b * p.a.N_cap + (j - e1)) * kD;
+                        else if (j < e3) src = p.kv_raw + ((size_t)rw.b * p.a.L_raw + rw.win_lo + (j - e2)) * kD;
                         cp_async16_or_zero(dst + half * kHalf + rr * 128 + ((cc ^ (rr & 7)) << 4), src + c16 * 8,
-                                           j < ow.len());
+                                           j < e3);
                     }
                     asm volatile("cp.async.commit_group;" ::: "memory");
                     settle(false);
@@ -370,30 +402,27 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             prefetch_tmap(&tm_q);
             constexpr uint32_t id_qk = idesc_bf16(kRows, kBN, false, false);
             constexpr uint32_t id_pv = idesc_bf16(kRows, kD, false, true);
-            int L0 = 0;                   // tiles of earlier units
-            int J[2] = {0, 0};            // tiles of each slot so far
-            int kO[2] = {0, 0};           // parts in which the slot had tiles
+            int ld0 = 0;                  // tiles of earlier units
+            uint32_t pp = 0;              // bit s: parity of slot s's next P
+            uint32_t po = 0;              // bit s: parity of slot s's next o_free (once it had a part)
+            uint32_t had = 0;             // bit s: slot s had tiles in an earlier part
             int nq = 0;                   // Q loads
             bool ok = true;
             if (p.stall) mbar_wait(&ctl->stall_bar, 0, abort, p.err, p.wait_ns);
             for (int u = u0; u < u1 && ok; ++u) {
-                const Geo g = geometry<G>(p, u);
+                const Geo g = geo[u - u0];
                 const Part pt = part_of(p, c, n_cta, u, g.total());
                 if (pt.lo >= pt.hi) continue;
-                if (*abort || (nq > 0 && !mbar_wait(&ctl->q_free, (nq - 1) & 1, abort, p.err, p.wait_ns))) { ok = false; break; }
+                if (*abort || (nq > 0 && !wait_bar(&ctl->q_free, (nq - 1) & 1, abort, p.err, p.wait_ns))) break;
                 mbar_arrive_expect_tx(&ctl->bar_q, 2 * kTileBytes);
                 for (int s = 0; s < 2; ++s)
                     for (int h = 0; h < 2; ++h)
                         tma_load_2d(sQ + s * kTileBytes + h * kHalf, &tm_q, h * 64, (2 * u + s) * kRows, &ctl->bar_q);
                 ++nq;
-                ok = mbar_wait(&ctl->bar_q, (nq - 1) & 1, abort, p.err, p.wait_ns);
-                auto next_of = [&](int s, int i) {        // the slot's first tile at or after i
-                    while (i < pt.hi && !((g.mask(i) >> s) & 1)) ++i;
-                    return i;
-                };
+                ok = wait_bar(&ctl->bar_q, (nq - 1) & 1, abort, p.err, p.wait_ns);
                 auto issue_qk = [&](int s, int i) -> bool {
-                    const int ld = L0 + i - pt.lo, slot = ld % kStages;
-                    if (!mbar_wait(&ctl->full[slot], (ld / kStages) & 1, abort, p.err, p.wait_ns)) return false;
+                    const int ld = ld0 + i - pt.lo, slot = ld % kStages;
+                    if (!wait_bar(&ctl->full[slot], (ld / kStages) & 1, abort, p.err, p.wait_ns)) return false;
                     tc_fence_after();
                     const uint64_t qd = sw128_desc(smem_u32(sQ + s * kTileBytes), 16, 1024);
                     const uint64_t kd = sw128_desc(smem_u32(sK + slot * kTileBytes), 16, 1024);
@@ -405,44 +434,55 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     mma_commit(&ctl->s_full[s]);
                     return true;
                 };
-                bool first[2] = {true, true};
-                int left = 0;                             // slots with Q.K still to issue
+                // nx0, nx1: the slots' next tiles to multiply with Q
+                int nx0 = g.next_of(0, pt.lo, pt.hi), nx1 = g.next_of(1, pt.lo, pt.hi);
+                uint32_t first = 3u;
                 for (int s = 0; s < 2 && ok; ++s) {
-                    const int i = next_of(s, pt.lo);
-                    if (i < pt.hi) {
-                        ++left;
-                        ok = issue_qk(s, i);
-                        if (ok && next_of(s, i + 1) >= pt.hi) --left;
-                    }
+                    const int i = s ? nx1 : nx0;
+                    if (i >= pt.hi) continue;
+                    ok = issue_qk(s, i);
+                    const int nx = g.next_of(s, i + 1, pt.hi);
+                    if (s) nx1 = nx;
+                    else nx0 = nx;
                 }
-                if (ok && left == 0) mma_commit(&ctl->q_free);
+                if (ok && nx0 >= pt.hi && nx1 >= pt.hi) mma_commit(&ctl->q_free);
                 for (int i = pt.lo; i < pt.hi && ok; ++i) {
-                    const int m = g.mask(i), slot = (L0 + i - pt.lo) % kStages;
-                    for (int s = 0; s < 2 && ok; ++s) {
+                    const int m = g.mask(i), slot = (ld0 + i - pt.lo) % kStages;
+#pragma unroll 1
+                    for (int s = 0; s < 2; ++s) {
                         if (!((m >> s) & 1)) continue;
-                        if (!mbar_wait(&ctl->p_ready[s], J[s] & 1, abort, p.err, p.wait_ns)) { ok = false; break; }
+                        ok = wait_bar(&ctl->p_ready[s], (pp >> s) & 1, abort, p.err, p.wait_ns);
+                        pp ^= 1u << s;
                         // the slot's previous O has been read
-                        if (first[s] && kO[s] > 0 && !mbar_wait(&ctl->o_free[s], (kO[s] - 1) & 1, abort, p.err, p.wait_ns)) { ok = false; break; }
+                        if (ok && ((first & had) >> s & 1)) {
+                            ok = wait_bar(&ctl->o_free[s], (po >> s) & 1, abort, p.err, p.wait_ns);
+                            po ^= 1u << s;
+                        }
+                        if (!ok) break;
                         tc_fence_after();
                         const uint64_t vd = sw128_desc(smem_u32(sK + slot * kTileBytes), kHalf, 1024);
+                        const uint32_t fresh = (first >> s) & 1;
 #pragma unroll
                         for (int kk = 0; kk < kBN / 16; ++kk)
                             mma_bf16_ts(tmem + 256 + s * 128, tmem + s * 128 + kk * 8, vd + (uint64_t)(kk * (2048 >> 4)),
-                                        id_pv, (!first[s] || kk > 0) ? 1u : 0u);
-                        first[s] = false;
-                        ++J[s];
+                                        id_pv, kk > 0 ? 1u : fresh ^ 1u);
+                        first &= ~(1u << s);
                         if ((m >> (s + 1)) == 0) mma_commit(&ctl->freeb[slot]);
-                        const int nx = next_of(s, i + 1);
+                        const int nx = s ? nx1 : nx0;
                         if (nx < pt.hi) {
                             ok = issue_qk(s, nx);
-                            if (ok && next_of(s, nx + 1) >= pt.hi && --left == 0) mma_commit(&ctl->q_free);
+                            if (!ok) break;
+                            const int after = g.next_of(s, nx + 1, pt.hi);
+                            if (s) nx1 = after;
+                            else nx0 = after;
+                            if (nx0 >= pt.hi && nx1 >= pt.hi) mma_commit(&ctl->q_free);
                         } else {
                             mma_commit(&ctl->o_full[s]);
-                            ++kO[s];
+                            had |= 1u << s;
                         }
                     }
                 }
-                L0 += pt.hi - pt.lo;
+                ld0 += pt.hi - pt.lo;
             }
             // every MMA must finish before TMEM is released, a Q load in
             // flight must land before shared memory is given up
@@ -463,11 +503,11 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         int J = 0, kO = 0;
         bool ok = true;
         for (int u = u0; u < u1 && ok; ++u) {
-            const Geo g = geometry<G>(p, u);
+            const Geo g = geo[u - u0];
             const Part pt = part_of(p, c, n_cta, u, g.total());
             const int qrow = (2 * u + s) * G + grp;
-            const Row row = row_of(p, qrow);
-            const int own_len = own_of(p, row, g.P * kBN).len();
+            const RowRec row = rows[((u - u0) * 2 + s) * G + grp];
+            const int own_len = row.n_pre + row.n_own + row.n_win;
             float m_used = -INFINITY, l_r = 0.0f, l_e = 0.0f;
             int n = 0;                                       // tiles of this part
             for (int i = pt.lo; i < pt.hi; ++i) {
@@ -479,63 +519,69 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     c_hi = c_lo + max(min(own_len - g.own_step(i) * H, H), 0);
                 }
                 // every wait is warp-collective: the TMEM accesses below are .sync.aligned
-                if (!__all_sync(0xffffffffu, mbar_wait(&ctl->s_full[s], J & 1, abort, p.err, p.wait_ns))) { ok = false; break; }
+                if (!__all_sync(0xffffffffu, wait_bar(&ctl->s_full[s], J & 1, abort, p.err, p.wait_ns))) { ok = false; break; }
                 ++J;
                 tc_fence_after();
-                float sv[kBN];
-                float mx0 = -INFINITY, mx1 = -INFINITY;
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    if (c_lo >= 32 * q + 32 || c_hi <= 32 * q) continue;
-                    tmem_ld32(s_addr + 32 * q, sv + 32 * q);
-                    if (c_hi < 32 * q + 32) {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (32 * q + e >= c_hi) sv[32 * q + e] = -INFINITY;
+                // One pass with the maximum in use; where a score outgrows it by more
+                // than 2^8 (and for a part's first tile) the maximum is raised and the
+                // pass repeated -- P is stored only at the end, so S is still there.
+                uint32_t pk[64];
+                bool seek = n == 0;                          // uniform in the warp
+                while (true) {
+                    if (seek) {
+                        const float mx = row_max(s_addr, c_lo, c_hi) * p.scale_log2;
+                        const bool raise = mx > m_used + kRescaleLog2;      // true for a row's first keys
+                        float alpha = 1.0f;
+                        if (raise) {
+                            alpha = (m_used == -INFINITY) ? 0.0f : ex2(m_used - mx);
+                            m_used = mx;
+                            l_r *= alpha;
+                            l_e *= alpha;
+                        }
+                        // (s_full of this tile was committed after the P.V of the one
+                        // before was issued, so that P.V has completed: O is stable)
+                        if (n > 0) rescale_o(o_addr, alpha);
                     }
+                    const float mm = (m_used == -INFINITY) ? 0.0f : m_used;
+                    const uint64_t sl2 = f2_pack(p.scale_log2, p.scale_log2), negm = f2_pack(-mm, -mm);
+                    uint64_t accr = 0, acce = 0;
+                    float zmax = -INFINITY;
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
-                        mx0 = max3(mx0, sv[32 * q + e], sv[32 * q + e + 1]);
-                        mx1 = max3(mx1, sv[32 * q + e + 2], sv[32 * q + e + 3]);
-                    }
-                }
-                const float mx = fmaxf(mx0, mx1) * p.scale_log2;
-                const bool raise = mx > m_used + kRescaleLog2;      // true for a row's first keys
-                float alpha = 1.0f;
-                if (raise) {
-                    alpha = (m_used == -INFINITY) ? 0.0f : ex2(m_used - mx);
-                    m_used = mx;
-                    l_r *= alpha;
-                    l_e *= alpha;
-                }
-                // (s_full of this tile was committed after the P.V of the one
-                // before was issued, so that P.V has completed: O is stable)
-                if (n > 0 && __any_sync(0xffffffffu, raise)) rescale_o(o_addr, alpha);
-                const float mm = (m_used == -INFINITY) ? 0.0f : m_used;
-                const uint64_t sl2 = f2_pack(p.scale_log2, p.scale_log2), negm = f2_pack(-mm, -mm);
-                uint64_t accr = 0, acce = 0;
+                    for (int q = 0; q < 4; ++q) {
+                        if (c_lo >= 32 * q + 32 || c_hi <= 32 * q) {
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    uint32_t pk[16];
-                    if (c_lo >= 32 * q + 32 || c_hi <= 32 * q) {
+                            for (int e = 0; e < 16; ++e) pk[16 * q + e] = 0u;
+                            continue;
+                        }
+                        float sv[32];
+                        tmem_ld32(s_addr + 32 * q, sv);
+                        if (c_hi < 32 * q + 32) {
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) pk[e] = 0u;
-                    } else {
+                            for (int e = 0; e < 32; ++e)
+                                if (32 * q + e >= c_hi) sv[e] = -INFINITY;
+                        }
 #pragma unroll
                         for (int e = 0; e < 32; e += 2) {
-                            const uint64_t z = f2_fma(f2_pack(sv[32 * q + e], sv[32 * q + e + 1]), sl2, negm);
+                            const uint64_t z = f2_fma(f2_pack(sv[e], sv[e + 1]), sl2, negm);
+                            zmax = max3(zmax, f2lo(z), f2hi(z));
                             const float p0 = ex2(f2lo(z)), p1 = ex2(f2hi(z));
                             uint32_t d;
                             asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(p1), "f"(p0));
-                            pk[e >> 1] = d;
+                            pk[16 * q + (e >> 1)] = d;
                             accr = f2_add(accr, f2_pack(__uint_as_float(d << 16), __uint_as_float(d & 0xffff0000u)));
                             if (LSE) acce = f2_add(acce, f2_pack(p0, p1));
                         }
                     }
-                    tmem_st16(s_addr + 16 * q, pk);
+                    if (!seek && __any_sync(0xffffffffu, zmax > kRescaleLog2 || (m_used == -INFINITY && zmax > -INFINITY))) {
+                        seek = true;
+                        continue;
+                    }
+                    l_r += f2lo(accr) + f2hi(accr);
+                    l_e += f2lo(acce) + f2hi(acce);
+                    break;
                 }
-                l_r += f2lo(accr) + f2hi(accr);
-                l_e += f2lo(acce) + f2hi(acce);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) tmem_st16(s_addr + 16 * q, pk + 16 * q);
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
@@ -545,7 +591,7 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             if (!ok) break;
             // ---------------------------------------------------------- the part's end
             if (n > 0) {
-                if (!__all_sync(0xffffffffu, mbar_wait(&ctl->o_full[s], kO & 1, abort, p.err, p.wait_ns))) break;
+                if (!__all_sync(0xffffffffu, wait_bar(&ctl->o_full[s], kO & 1, abort, p.err, p.wait_ns))) break;
                 ++kO;
                 tc_fence_after();
             }
@@ -717,7 +763,7 @@ Plan plan_of(const AttnArgs& a) {
     const long own = (std::min<long>(kBN, a.N_p) + a.N_cap + a.window + a.H - 1) / a.H;
     const long T = std::max<long>(a.N_p / kBN + (p.R > per / 2 ? 2 : 1) * own, 1);
     if (p.U >= kSms) {
-        p.n_cta = kSms;
+        p.n_cta = std::max(kSms, (p.U + kMaxUnits - 3) / (kMaxUnits - 2));
     } else {
         // as many whole cuts of every unit as fit one wave, no cut below one
         // tile; or an uneven cut over all SMs, whose CTAs meet two units and
