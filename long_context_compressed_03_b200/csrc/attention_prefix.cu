@@ -63,8 +63,8 @@ constexpr int kTileBytes = 2 * kHalf;
 constexpr int kLoadWarps = 3;
 constexpr int kLoadThreads = kLoadWarps * 32;
 constexpr int kMmaWarp = kLoadWarps;
-constexpr int kSoftWarp0 = 4;
-constexpr int kThreads = 12 * 32;
+constexpr int kSoftWarp0 = 4;                // 8 softmax warps a slot
+constexpr int kThreads = (kSoftWarp0 + 16) * 32;
 constexpr int kSms = 148;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescaleLog2 = 8.0f;
@@ -77,6 +77,9 @@ struct __align__(8) Ctrl {
     uint64_t fin, stall_bar;
     uint32_t tmem_base;
     int abort;
+    // between the two threads of a row: maximum, sums of rounded / exact weights
+    float xm[2][2][kRows];
+    float xl[2][2][2][2][kRows];             // (by unit parity)
 };
 
 struct PrefixParams {
@@ -113,6 +116,8 @@ struct RowRec {
 struct Geo {
     int P, T0, T1;
     int on;                  // bit s: slot s has a row with a position
+    // the CTA's part of the list: tiles [lo, hi); the unit's part number; all of it?
+    int lo, hi, ord, whole;
     __device__ __forceinline__ int total() const { return P + T0 + T1; }
     __device__ __forceinline__ int own_slot(int i) const {
         const int j = i - P, both = 2 * min(T0, T1);
@@ -124,8 +129,8 @@ struct Geo {
     }
     // bit s: slot s uses tile i
     __device__ __forceinline__ int mask(int i) const { return i < P ? on : 1 << own_slot(i); }
-    // the first tile of slot s at or after i (hi: none below it)
-    __device__ __forceinline__ int next_of(int s, int i, int hi) const {
+    // the part's first tile of slot s at or after i (hi: none)
+    __device__ __forceinline__ int next_of(int s, int i) const {
         if (i < P) {
             if ((on >> s) & 1) return min(i, hi);
             i = P;
@@ -142,7 +147,8 @@ constexpr int kMaxUnits = 32;            // units a CTA meets, at most
 
 // The CTA's units u0 .. u0 + n - 1: a thread per query row, then one per unit.
 template <int G>
-__device__ __forceinline__ void fill_geometry(const PrefixParams& p, int u0, int n, Geo* geo, RowRec* rows) {
+__device__ __forceinline__ void fill_geometry(const PrefixParams& p, int c, int n_cta, int u0, int n, Geo* geo,
+                                              RowRec* rows) {
     for (int i = threadIdx.x; i < n * 2 * G; i += kThreads) {
         const int row = u0 * 2 * G + i;
         RowRec r{};
@@ -161,7 +167,7 @@ __device__ __forceinline__ void fill_geometry(const PrefixParams& p, int u0, int
     }
     __syncthreads();
     for (int k = threadIdx.x; k < n; k += kThreads) {
-        Geo g{0, 0, 0, 0};
+        Geo g{};
         int lo = p.a.N_p;
 #pragma unroll
         for (int i = 0; i < 2 * G; ++i) {
@@ -182,24 +188,16 @@ __device__ __forceinline__ void fill_geometry(const PrefixParams& p, int u0, int
             if (i < G) g.T0 = max(g.T0, T);
             else g.T1 = max(g.T1, T);
         }
+        // CTA c takes [c U, (c+1) U) of the line on which unit u is [u n_cta, (u+1) n_cta)
+        const long a = (long)c * p.U, b = a + p.U, x = (long)(u0 + k) * n_cta, y = x + n_cta;
+        g.lo = (int)((max(a, x) - x) * g.total() / n_cta);
+        g.hi = (int)((min(b, y) - x) * g.total() / n_cta);
+        g.ord = c - (int)(x / p.U);
+        g.whole = a <= x && b >= y;
         geo[k] = g;
     }
 }
 
-// The part of unit u that CTA c of n takes, as a range of its tile list.
-struct Part {
-    int lo, hi, ord;         // ord: which of the unit's parts
-    bool whole;
-};
-__device__ __forceinline__ Part part_of(const PrefixParams& p, int c, int n, int u, int T) {
-    const long a = (long)c * p.U, b = a + p.U, x = (long)u * n, y = x + n;
-    Part r;
-    r.lo = (int)((max(a, x) - x) * T / n);
-    r.hi = (int)((min(b, y) - x) * T / n);
-    r.ord = c - (int)(x / p.U);
-    r.whole = a <= x && b >= y;
-    return r;
-}
 __device__ __forceinline__ int first_unit(const PrefixParams& p, int c, int n) { return (int)((long)c * p.U / n); }
 __device__ __forceinline__ int end_unit(const PrefixParams& p, int c, int n) {
     return (int)(((long)(c + 1) * p.U + n - 1) / n);
@@ -244,37 +242,20 @@ __device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
 __device__ __forceinline__ float f2lo(uint64_t v) { return __uint_as_float((uint32_t)v); }
 __device__ __forceinline__ float f2hi(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
 
+// Adds bytes that the barrier's current phase waits for, without arriving.
+__device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
+    asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
+}
 // 16-byte copy global -> shared, or 16 zero bytes (nothing is read) when !on.
 __device__ __forceinline__ void cp_async16_or_zero(void* dst, const void* src, bool on) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
                  ::"r"(smem_u32(dst)), "l"(src), "r"(on ? 16 : 0) : "memory");
 }
 
-// Largest S of the row's columns [c_lo, c_hi) (c_lo a multiple of 32; uniform in a warp).
-__device__ __noinline__ float row_max(uint32_t s_addr, int c_lo, int c_hi) {
-    float mx0 = -INFINITY, mx1 = -INFINITY;
-#pragma unroll 1
-    for (int c = c_lo; c < c_hi; c += 32) {
-        float sv[32];
-        tmem_ld32(s_addr + c, sv);
-        if (c_hi < c + 32) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-                if (c + e >= c_hi) sv[e] = -INFINITY;
-        }
-#pragma unroll
-        for (int e = 0; e < 32; e += 4) {
-            mx0 = max3(mx0, sv[e], sv[e + 1]);
-            mx1 = max3(mx1, sv[e + 2], sv[e + 3]);
-        }
-    }
-    return fmaxf(mx0, mx1);
-}
-
-// The row maximum grew by more than 2^8: rescale the row's O in TMEM.
+// The row maximum grew by more than 2^8: rescale this thread's half of the row's O.
 __device__ __noinline__ void rescale_o(uint32_t o_addr, float alpha) {
 #pragma unroll 1
-    for (int q = 0; q < 4; ++q) {
+    for (int q = 0; q < 2; ++q) {
         float ov[32];
         tmem_ld32(o_addr + q * 32, ov);
 #pragma unroll
@@ -285,8 +266,9 @@ __device__ __noinline__ void rescale_o(uint32_t o_addr, float alpha) {
 }
 
 template <int G, bool LSE>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __maxnreg__(96)
 attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_p,
+                   const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ CUtensorMap tm_w,
                    const __grid_constant__ PrefixParams p) {
     constexpr int H = kRows / G;
     extern __shared__ uint8_t smem_raw[];
@@ -310,9 +292,9 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&ctl->s_full[i], 1);
-            mbar_init(&ctl->p_ready[i], 4);
+            mbar_init(&ctl->p_ready[i], 8);
             mbar_init(&ctl->o_full[i], 1);
-            mbar_init(&ctl->o_free[i], 4);
+            mbar_init(&ctl->o_free[i], 8);
         }
         mbar_init(&ctl->fin, 1);
         mbar_init(&ctl->stall_bar, 1);
@@ -324,7 +306,7 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         tmem_alloc(&ctl->tmem_base, 512);
         tmem_relinquish();
     }
-    fill_geometry<G>(p, u0, u1 - u0, geo, rows);
+    fill_geometry<G>(p, c, n_cta, u0, u1 - u0, geo, rows);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -332,11 +314,11 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 
     if (warp < kLoadWarps) {
         // ------------------------------------------------------------ key tiles
-        const int lt = threadIdx.x, c16 = lt & 15, half = c16 >> 3, cc = c16 & 7;
+        const int lt = threadIdx.x, c16 = lt & 15;
+        const uint32_t col = (uint32_t)(c16 >> 3) * kHalf;   // this thread's 16 bytes of a row
         int L = 0;                    // tiles handed out
         int pend = -1;                // stage of a copied tile that has not arrived yet
-        uint32_t tma_stage = 0;       // stages whose latest tile came by TMA (thread 0's)
-        bool ok = true;
+        uint32_t tma_stage = 0;       // stages whose latest tile came (in part) by TMA
         // the copied tile before the latest commit group has landed: hand it over
         auto settle = [&](bool all) {
             if (all) asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -347,85 +329,108 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 pend = -1;
             }
         };
+        bool ok = true;
         for (int u = u0; u < u1 && ok; ++u) {
             const Geo g = geo[u - u0];
-            const Part pt = part_of(p, c, n_cta, u, g.total());
-            for (int i = pt.lo; i < pt.hi; ++i, ++L) {
+            for (int i = g.lo; i < g.hi; ++i, ++L) {
                 const int slot = L % kStages, use = L / kStages;
                 if (use > 0 && !wait_bar(&ctl->freeb[slot], (use - 1) & 1, abort, p.err, p.wait_ns)) { ok = false; break; }
                 if (*abort) { ok = false; break; }
                 uint8_t* dst = sK + slot * kTileBytes;
-                if (i < g.P) {
+                uint64_t* bar = &ctl->full[slot];
+                // the tile as 128 / N runs of N rows: contiguous rows come by TMA boxes of 64
+                const bool shared = i < g.P;
+                const int ms = shared ? 0 : g.own_slot(i), j0 = shared ? 0 : g.own_step(i) * H;
+                const RowRec* rec = rows + ((u - u0) * 2 + ms) * G;
+                bool copies = false;
+                uint32_t boxes = 0;
+                if (shared) {
+                    boxes = 4;
                     if (lt == 0) {
-                        mbar_arrive_expect_tx(&ctl->full[slot], kTileBytes);
-                        tma_load_2d(dst, &tm_p, 0, i * kBN, &ctl->full[slot]);
-                        tma_load_2d(dst + kHalf, &tm_p, 64, i * kBN, &ctl->full[slot]);
-                        tma_stage |= 1u << slot;
-                    } else {
-                        mbar_arrive(&ctl->full[slot]);
+                        mbar_expect_tx(bar, kTileBytes);
+                        for (int k = 0; k < 4; ++k)
+                            tma_load_2d(dst + (k & 1) * kHalf + (k >> 1) * 8192, &tm_p, (k & 1) * 64, i * kBN + (k >> 1) * 64, bar);
                     }
-                    asm volatile("cp.async.commit_group;" ::: "memory");
-                    settle(false);
                 } else {
-                    if (lt == 0) tma_stage &= ~(1u << slot);
-                    const int ms = g.own_slot(i), j0 = g.own_step(i) * H;
-                    const RowRec* rec = rows + ((u - u0) * 2 + ms) * G;
-#pragma unroll 2
-                    for (int rr = lt >> 4; rr < kBN; rr += kLoadThreads / 16) {
-                        const int k = rr / H, j = j0 + rr % H;
-                        const RowRec rw = rec[k];
-                        const __nv_bfloat16* src = p.out;          // any address: nothing is read past the list
-                        const int e1 = rw.n_pre, e2 = e1 + rw.n_own, e3 = e2 + rw.n_win;
-                        if (j < e1) src = p.kv_p + (size_t)(g.P * kBN + j) * kD;
-                        else if (j < e2) src = p.kv_c + ((size_t)rw.b * p.a.N_cap + (j - e1)) * kD;
-                        else if (j < e3) src = p.kv_raw + ((size_t)rw.b * p.a.L_raw + rw.win_lo + (j - e2)) * kD;
-                        cp_async16_or_zero(dst + half * kHalf + rr * 128 + ((cc ^ (rr & 7)) << 4), src + c16 * 8,
-                                           j < e3);
+#pragma unroll
+                    for (int k = 0; k < kBN / 64; ++k) {          // 64 rows of the tile
+                        const RowRec rw = rec[G == 2 ? k : 0];
+                        const int j = j0 + (G == 2 ? 0 : 64 * k);
+                        const int e1 = rw.n_win, e2 = e1 + rw.n_pre, e3 = e2 + rw.n_own;
+                        // one segment holds all 64 rows: window, rest of the prefix, own entries
+                        const bool w = j + 64 <= e1, pre = j >= e1 && j + 64 <= e2, own = j >= e2 && j + 64 <= e3;
+                        if (w || pre || own) {
+                            boxes += 2;
+                            if (lt == 0) {
+                                const CUtensorMap* m = w ? &tm_w : (pre ? &tm_p : &tm_c);
+                                const int y = w ? rw.b * p.a.L_raw + rw.win_lo + j
+                                                : (pre ? g.P * kBN + (j - e1) : rw.b * p.a.N_cap + (j - e2));
+                                mbar_expect_tx(bar, 2 * 8192);
+                                tma_load_2d(dst + k * 8192, m, 0, y, bar);
+                                tma_load_2d(dst + kHalf + k * 8192, m, 64, y, bar);
+                            }
+                            continue;
+                        }
+                        // row by row, zero rows past the list's end
+                        copies = true;
+#pragma unroll 1
+                        for (int rr = lt >> 4; rr < 64; rr += kLoadThreads / 16) {
+                            const int jj = j + rr;
+                            const __nv_bfloat16* src = p.out;      // any address: nothing is read past the end
+                            if (jj < e1) src = p.kv_raw + ((size_t)rw.b * p.a.L_raw + rw.win_lo + jj) * kD;
+                            else if (jj < e2) src = p.kv_p + (size_t)(g.P * kBN + (jj - e1)) * kD;
+                            else if (jj < e3) src = p.kv_c + ((size_t)rw.b * p.a.N_cap + (jj - e2)) * kD;
+                            cp_async16_or_zero(dst + col + (64 * k + rr) * 128 + (((c16 & 7) ^ (rr & 7)) << 4), src + c16 * 8,
+                                               jj < e3);
+                        }
                     }
-                    asm volatile("cp.async.commit_group;" ::: "memory");
-                    settle(false);
-                    pend = slot;
                 }
+                if (boxes) tma_stage |= 1u << slot;
+                else tma_stage &= ~(1u << slot);
+                asm volatile("cp.async.commit_group;" ::: "memory");
+                settle(false);
+                if (copies) pend = slot;
+                else mbar_arrive(bar);
             }
         }
         settle(true);
         // TMA tiles in flight land before the CTA's shared memory is given up
         if (lt == 0) {
             volatile int never = 0;
-            for (int s = 0; s < kStages; ++s)
-                if (((tma_stage >> s) & 1u) && L > s)
-                    mbar_wait(&ctl->full[s], ((L - 1 - s) / kStages) & 1, &never, p.err);
+            for (int k = 0; k < kStages; ++k)
+                if (((tma_stage >> k) & 1u) && L > k)
+                    mbar_wait(&ctl->full[k], ((L - 1 - k) / kStages) & 1, &never, p.err);
         }
     } else if (warp == kMmaWarp) {
         // ------------------------------------------------------------ Q and every MMA
         if (lane == 0) {
-            prefetch_tmap(&tm_q);
             constexpr uint32_t id_qk = idesc_bf16(kRows, kBN, false, false);
             constexpr uint32_t id_pv = idesc_bf16(kRows, kD, false, true);
+            const uint64_t qd0 = sw128_desc(smem_u32(sQ), 16, 1024), kd0 = sw128_desc(smem_u32(sK), 16, 1024);
+            const uint64_t vd0 = sw128_desc(smem_u32(sK), kHalf, 1024);
             int ld0 = 0;                  // tiles of earlier units
             uint32_t pp = 0;              // bit s: parity of slot s's next P
             uint32_t po = 0;              // bit s: parity of slot s's next o_free (once it had a part)
             uint32_t had = 0;             // bit s: slot s had tiles in an earlier part
-            int nq = 0;                   // Q loads
+            int nq = 0, nfree = 0;        // Q loads; parts whose Q was used up
             bool ok = true;
             if (p.stall) mbar_wait(&ctl->stall_bar, 0, abort, p.err, p.wait_ns);
             for (int u = u0; u < u1 && ok; ++u) {
                 const Geo g = geo[u - u0];
-                const Part pt = part_of(p, c, n_cta, u, g.total());
-                if (pt.lo >= pt.hi) continue;
-                if (*abort || (nq > 0 && !wait_bar(&ctl->q_free, (nq - 1) & 1, abort, p.err, p.wait_ns))) break;
+                if (g.lo >= g.hi) continue;
+                if (*abort || (nfree > 0 && !wait_bar(&ctl->q_free, (nfree - 1) & 1, abort, p.err, p.wait_ns))) break;
                 mbar_arrive_expect_tx(&ctl->bar_q, 2 * kTileBytes);
-                for (int s = 0; s < 2; ++s)
-                    for (int h = 0; h < 2; ++h)
-                        tma_load_2d(sQ + s * kTileBytes + h * kHalf, &tm_q, h * 64, (2 * u + s) * kRows, &ctl->bar_q);
+                for (int k = 0; k < 8; ++k)
+                    tma_load_2d(sQ + (k >> 1) * 8192 + (k & 1) * kHalf + (k >> 2) * kHalf, &tm_q, (k & 1) * 64,
+                                2 * u * kRows + (k >> 1) * 64, &ctl->bar_q);
                 ++nq;
                 ok = wait_bar(&ctl->bar_q, (nq - 1) & 1, abort, p.err, p.wait_ns);
-                auto issue_qk = [&](int s, int i) -> bool {
-                    const int ld = ld0 + i - pt.lo, slot = ld % kStages;
+                // S of slot s = Q . tile `ld` of the CTA
+                auto issue_qk = [&](int s, int ld) -> bool {
+                    const int slot = ld % kStages;
                     if (!wait_bar(&ctl->full[slot], (ld / kStages) & 1, abort, p.err, p.wait_ns)) return false;
                     tc_fence_after();
-                    const uint64_t qd = sw128_desc(smem_u32(sQ + s * kTileBytes), 16, 1024);
-                    const uint64_t kd = sw128_desc(smem_u32(sK + slot * kTileBytes), 16, 1024);
+                    const uint64_t qd = qd0 + (uint64_t)(s * (kTileBytes >> 4)), kd = kd0 + (uint64_t)(slot * (kTileBytes >> 4));
 #pragma unroll
                     for (int kq = 0; kq < kD / 16; ++kq) {
                         const uint32_t off16 = ((kq >> 2) * kHalf + (kq & 3) * 32) >> 4;
@@ -434,55 +439,52 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     mma_commit(&ctl->s_full[s]);
                     return true;
                 };
-                // nx0, nx1: the slots' next tiles to multiply with Q
-                int nx0 = g.next_of(0, pt.lo, pt.hi), nx1 = g.next_of(1, pt.lo, pt.hi);
-                uint32_t first = 3u;
+                const int ldx = ld0 - g.lo;               // tile i of the list is the CTA's tile ldx + i
                 for (int s = 0; s < 2 && ok; ++s) {
-                    const int i = s ? nx1 : nx0;
-                    if (i >= pt.hi) continue;
-                    ok = issue_qk(s, i);
-                    const int nx = g.next_of(s, i + 1, pt.hi);
-                    if (s) nx1 = nx;
-                    else nx0 = nx;
+                    const int i = g.next_of(s, g.lo);
+                    if (i < g.hi) ok = issue_qk(s, ldx + i);
                 }
-                if (ok && nx0 >= pt.hi && nx1 >= pt.hi) mma_commit(&ctl->q_free);
-                for (int i = pt.lo; i < pt.hi && ok; ++i) {
-                    const int m = g.mask(i), slot = (ld0 + i - pt.lo) % kStages;
+                const int dual_end = g.on == 3 ? min(g.P, g.hi) : 0;    // tiles below it serve both slots
+                uint32_t first = 3u;
 #pragma unroll 1
-                    for (int s = 0; s < 2; ++s) {
-                        if (!((m >> s) & 1)) continue;
+                for (int i = g.lo, s = 0; i < g.hi && ok;) {
+                    // slot s's P of tile i: O += P . V, then its next Q . K
+                    const int m = i < dual_end ? 3 : g.mask(i);
+                    const bool last = s == 1 || m == 1;   // the tile's last use
+                    if ((m >> s) & 1) {
+                        const int slot = (ldx + i) % kStages;
+                        const int nx = i + 1 < dual_end ? i + 1 : g.next_of(s, i + 1);
                         ok = wait_bar(&ctl->p_ready[s], (pp >> s) & 1, abort, p.err, p.wait_ns);
                         pp ^= 1u << s;
-                        // the slot's previous O has been read
-                        if (ok && ((first & had) >> s & 1)) {
+                        if (ok && ((first & had) >> s & 1)) {          // the slot's previous O has been read
                             ok = wait_bar(&ctl->o_free[s], (po >> s) & 1, abort, p.err, p.wait_ns);
                             po ^= 1u << s;
                         }
                         if (!ok) break;
                         tc_fence_after();
-                        const uint64_t vd = sw128_desc(smem_u32(sK + slot * kTileBytes), kHalf, 1024);
-                        const uint32_t fresh = (first >> s) & 1;
+                        const uint64_t vd = vd0 + (uint64_t)(slot * (kTileBytes >> 4));
+                        const uint32_t acc = ((first >> s) & 1) ^ 1u;
 #pragma unroll
                         for (int kk = 0; kk < kBN / 16; ++kk)
-                            mma_bf16_ts(tmem + 256 + s * 128, tmem + s * 128 + kk * 8, vd + (uint64_t)(kk * (2048 >> 4)),
-                                        id_pv, kk > 0 ? 1u : fresh ^ 1u);
+                            mma_bf16_ts(tmem + 256 + s * 128, tmem + s * 128 + (kk >> 2) * 64 + (kk & 3) * 8, vd + (uint64_t)(kk * (2048 >> 4)),
+                                        id_pv, kk > 0 ? 1u : acc);
                         first &= ~(1u << s);
-                        if ((m >> (s + 1)) == 0) mma_commit(&ctl->freeb[slot]);
-                        const int nx = s ? nx1 : nx0;
-                        if (nx < pt.hi) {
-                            ok = issue_qk(s, nx);
-                            if (!ok) break;
-                            const int after = g.next_of(s, nx + 1, pt.hi);
-                            if (s) nx1 = after;
-                            else nx0 = after;
-                            if (nx0 >= pt.hi && nx1 >= pt.hi) mma_commit(&ctl->q_free);
+                        if (last) mma_commit(&ctl->freeb[slot]);
+                        if (nx < g.hi) {
+                            ok = issue_qk(s, ldx + nx);
                         } else {
                             mma_commit(&ctl->o_full[s]);
                             had |= 1u << s;
                         }
                     }
+                    i += last;
+                    s = last ? 0 : 1;
                 }
-                ld0 += pt.hi - pt.lo;
+                if (ok) {
+                    mma_commit(&ctl->q_free);
+                    ++nfree;
+                }
+                ld0 += g.hi - g.lo;
             }
             // every MMA must finish before TMEM is released, a Q load in
             // flight must land before shared memory is given up
@@ -494,94 +496,117 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         __syncwarp();
     } else {
         // ------------------------------------------------------------ softmax and output
-        const int s = (warp - kSoftWarp0) >> 2;
+        // A row belongs to two threads, one per 64-column half of S (and of O).
+        const int s = (warp - kSoftWarp0) >> 3, h = ((warp - kSoftWarp0) >> 2) & 1;
         const int r = (warp & 3) * 32 + lane;                // row of the M tile
         const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t s_addr = tmem + lane_addr + s * 128;
-        const uint32_t o_addr = tmem + lane_addr + 256 + s * 128;
+        const uint32_t o_addr = tmem + lane_addr + 256 + s * 128 + 64 * h;
         const int grp = r / H;                               // the row's query row in the slot
-        int J = 0, kO = 0;
+        // The row's two warps meet here once per tile; the result is the OR of
+        // both warps' flags.  A warp whose wait ran out comes too, so neither is
+        // left waiting; the abort flag is set before it comes.
+        const int pair_id = 1 + s * 4 + (warp & 3);
+        auto pair_or = [&](bool flag) -> bool {
+            uint32_t any;
+            asm volatile("{\n\t.reg .pred q, r;\n\t"
+                         "setp.ne.u32 q, %1, 0;\n\t"
+                         "barrier.cta.red.or.pred r, %2, 64, q;\n\t"
+                         "selp.u32 %0, 1, 0, r;\n\t}"
+                         : "=r"(any) : "r"((uint32_t)flag), "r"(pair_id) : "memory");
+            return any != 0;
+        };
+        uint32_t ps = 0, po = 0;                             // parities of s_full, o_full
         bool ok = true;
         for (int u = u0; u < u1 && ok; ++u) {
             const Geo g = geo[u - u0];
-            const Part pt = part_of(p, c, n_cta, u, g.total());
             const int qrow = (2 * u + s) * G + grp;
             const RowRec row = rows[((u - u0) * 2 + s) * G + grp];
             const int own_len = row.n_pre + row.n_own + row.n_win;
             float m_used = -INFINITY, l_r = 0.0f, l_e = 0.0f;
             int n = 0;                                       // tiles of this part
-            for (int i = pt.lo; i < pt.hi; ++i) {
+#pragma unroll 1
+            for (int i = g.lo; i < g.hi; ++i) {
                 if (!((g.mask(i) >> s) & 1)) continue;
-                // columns of this row: all, or [c_lo, c_hi) of its H columns (uniform in a warp)
-                int c_lo = 0, c_hi = kBN;
+                // this half's columns that are keys of the row (the same in all lanes)
+                int nv = 64;
                 if (i >= g.P) {
-                    c_lo = grp * H;
-                    c_hi = c_lo + max(min(own_len - g.own_step(i) * H, H), 0);
+                    nv = own_len - g.own_step(i) * H - (G == 1 ? 64 * h : 0);
+                    nv = (G == 2 && h != grp) ? 0 : max(min(nv, 64), 0);
                 }
                 // every wait is warp-collective: the TMEM accesses below are .sync.aligned
-                if (!__all_sync(0xffffffffu, wait_bar(&ctl->s_full[s], J & 1, abort, p.err, p.wait_ns))) { ok = false; break; }
-                ++J;
+                ok = __all_sync(0xffffffffu, wait_bar(&ctl->s_full[s], ps, abort, p.err, p.wait_ns));
+                ps ^= 1;
                 tc_fence_after();
-                // One pass with the maximum in use; where a score outgrows it by more
-                // than 2^8 (and for a part's first tile) the maximum is raised and the
-                // pass repeated -- P is stored only at the end, so S is still there.
-                uint32_t pk[64];
-                bool seek = n == 0;                          // uniform in the warp
-                while (true) {
-                    if (seek) {
-                        const float mx = row_max(s_addr, c_lo, c_hi) * p.scale_log2;
-                        const bool raise = mx > m_used + kRescaleLog2;      // true for a row's first keys
-                        float alpha = 1.0f;
-                        if (raise) {
-                            alpha = (m_used == -INFINITY) ? 0.0f : ex2(m_used - mx);
-                            m_used = mx;
-                            l_r *= alpha;
-                            l_e *= alpha;
-                        }
-                        // (s_full of this tile was committed after the P.V of the one
-                        // before was issued, so that P.V has completed: O is stable)
-                        if (n > 0) rescale_o(o_addr, alpha);
+                if (!ok) {
+                    pair_or(true);
+                    break;
+                }
+                float sv[64];
+                for (bool again = false;; again = true) {
+                    tmem_ld64(s_addr + 64 * h, sv);
+                    if (nv < 64) {
+#pragma unroll
+                        for (int e = 0; e < 64; ++e)
+                            if (e >= nv) sv[e] = -INFINITY;
                     }
+                    float mx = -INFINITY, mx1 = -INFINITY;
+#pragma unroll
+                    for (int e = 0; e < 64; e += 4) {
+                        mx = max3(mx, sv[e], sv[e + 1]);
+                        mx1 = max3(mx1, sv[e + 2], sv[e + 3]);
+                    }
+                    mx = fmaxf(mx, mx1) * p.scale_log2;
+                    // the maximum in use is raised (and O rescaled) where a score outgrows
+                    // it by more than 2^8; true for a row's first keys
+                    if (again || !pair_or(mx > m_used + kRescaleLog2)) break;
+                    ok = *abort == 0;
+                    if (!ok) break;
+                    ctl->xm[s][h][r] = mx;
+                    pair_or(false);
+                    mx = fmaxf(mx, ctl->xm[s][h ^ 1][r]);
+                    float alpha = 1.0f;
+                    if (mx > m_used + kRescaleLog2) {
+                        alpha = (m_used == -INFINITY) ? 0.0f : ex2(m_used - mx);
+                        m_used = mx;
+                        l_r *= alpha;
+                        l_e *= alpha;
+                    }
+                    // (s_full of this tile was committed after the P.V of the one
+                    // before was issued, so that P.V has completed: O is stable.)
+                    // S is read again rather than kept in registers across the call.
+                    if (n > 0) rescale_o(o_addr, alpha);
+                }
+                if (!ok) break;
+                // P of this half's 64 keys, over the S it was made from
+                if (nv > 0) {
                     const float mm = (m_used == -INFINITY) ? 0.0f : m_used;
                     const uint64_t sl2 = f2_pack(p.scale_log2, p.scale_log2), negm = f2_pack(-mm, -mm);
                     uint64_t accr = 0, acce = 0;
-                    float zmax = -INFINITY;
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        if (c_lo >= 32 * q + 32 || c_hi <= 32 * q) {
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) pk[16 * q + e] = 0u;
-                            continue;
-                        }
-                        float sv[32];
-                        tmem_ld32(s_addr + 32 * q, sv);
-                        if (c_hi < 32 * q + 32) {
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                if (32 * q + e >= c_hi) sv[e] = -INFINITY;
-                        }
+                    for (int q = 0; q < 2; ++q) {
+                        uint32_t pk[16];
 #pragma unroll
                         for (int e = 0; e < 32; e += 2) {
-                            const uint64_t z = f2_fma(f2_pack(sv[e], sv[e + 1]), sl2, negm);
-                            zmax = max3(zmax, f2lo(z), f2hi(z));
+                            const uint64_t z = f2_fma(f2_pack(sv[32 * q + e], sv[32 * q + e + 1]), sl2, negm);
                             const float p0 = ex2(f2lo(z)), p1 = ex2(f2hi(z));
                             uint32_t d;
                             asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(p1), "f"(p0));
-                            pk[16 * q + (e >> 1)] = d;
+                            pk[e >> 1] = d;
                             accr = f2_add(accr, f2_pack(__uint_as_float(d << 16), __uint_as_float(d & 0xffff0000u)));
                             if (LSE) acce = f2_add(acce, f2_pack(p0, p1));
                         }
-                    }
-                    if (!seek && __any_sync(0xffffffffu, zmax > kRescaleLog2 || (m_used == -INFINITY && zmax > -INFINITY))) {
-                        seek = true;
-                        continue;
+                        tmem_st16(s_addr + 64 * h + 16 * q, pk);
                     }
                     l_r += f2lo(accr) + f2hi(accr);
                     l_e += f2lo(acce) + f2hi(acce);
-                    break;
-                }
+                } else {
+                    uint32_t zero[16];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) tmem_st16(s_addr + 16 * q, pk + 16 * q);
+                    for (int e = 0; e < 16; ++e) zero[e] = 0u;
+                    tmem_st16(s_addr + 64 * h, zero);
+                    tmem_st16(s_addr + 64 * h + 16, zero);
+                }
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
@@ -591,23 +616,28 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             if (!ok) break;
             // ---------------------------------------------------------- the part's end
             if (n > 0) {
-                if (!__all_sync(0xffffffffu, wait_bar(&ctl->o_full[s], kO & 1, abort, p.err, p.wait_ns))) break;
-                ++kO;
+                ok = __all_sync(0xffffffffu, wait_bar(&ctl->o_full[s], po, abort, p.err, p.wait_ns));
+                po ^= 1;
                 tc_fence_after();
             }
+            ctl->xl[u & 1][s][h][0][r] = l_r;
+            ctl->xl[u & 1][s][h][1][r] = l_e;
+            if (pair_or(!ok)) { ok = false; break; }
+            l_r += ctl->xl[u & 1][s][h ^ 1][0][r];
+            l_e += ctl->xl[u & 1][s][h ^ 1][1][r];
             const long orow = (long)(2 * u + s) * kRows + r;         // flattened (row, head)
             const bool row_ok = qrow < p.R;
             if (!row.on) {               // no position: no key, whatever the shared tiles held
                 m_used = -INFINITY;
                 l_r = l_e = 0.0f;
             }
-            if (pt.whole) {
-                __nv_bfloat16* dst = p.out + orow * kD;
+            if (g.whole) {
+                __nv_bfloat16* dst = p.out + orow * kD + 64 * h;
                 const float inv = (l_r == 0.0f) ? 0.0f : 1.0f / l_r;
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
+#pragma unroll 1
+                for (int q = 0; q < 2; ++q) {
                     float ov[32];
-                    if (n > 0) tmem_ld32(o_addr + q * 32, ov);
+                    tmem_ld32(o_addr + q * 32, ov);          // (nothing of it is used without keys)
                     if (row_ok) {
 #pragma unroll
                         for (int e = 0; e < 32; e += 8) {
@@ -624,24 +654,26 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         }
                     }
                 }
-                if (LSE && row_ok) p.lse[orow] = (l_e == 0.0f) ? -INFINITY : (m_used + log2f(l_e)) / kLog2e;
+                if (LSE && row_ok && h == 0) p.lse[orow] = (l_e == 0.0f) ? -INFINITY : (m_used + log2f(l_e)) / kLog2e;
             } else {
                 // O as [column quad][row] of float4: lanes (rows) are consecutive
-                float* ws = p.ws + ((size_t)(u * p.parts + pt.ord) * 2 + s) * kPartFloats;
-                if (n > 0) {
+                float* ws = p.ws + ((size_t)(u * p.parts + g.ord) * 2 + s) * kPartFloats;
+                {
 #pragma unroll 1
-                    for (int q = 0; q < 4; ++q) {
+                    for (int q = 0; q < 2; ++q) {
                         float ov[32];
                         tmem_ld32(o_addr + q * 32, ov);
 #pragma unroll
                         for (int e = 0; e < 32; e += 4)
-                            *reinterpret_cast<float4*>(ws + ((q * 8 + (e >> 2)) * kRows + r) * 4) =
+                            *reinterpret_cast<float4*>(ws + ((h * 16 + q * 8 + (e >> 2)) * kRows + r) * 4) =
                                 make_float4(ov[e], ov[e + 1], ov[e + 2], ov[e + 3]);
                     }
                 }
-                ws[kRows * kD + r] = n > 0 ? m_used : -INFINITY;
-                ws[kRows * kD + kRows + r] = l_r;
-                ws[kRows * kD + 2 * kRows + r] = l_e;
+                if (h == 0) {
+                    ws[kRows * kD + r] = n > 0 ? m_used : -INFINITY;
+                    ws[kRows * kD + kRows + r] = l_r;
+                    ws[kRows * kD + 2 * kRows + r] = l_e;
+                }
             }
             if (n > 0) {
                 tc_fence_before();
@@ -660,67 +692,56 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 }
 
 // ---------------------------------------------------------------------- join
-// One CTA per slot of a cut unit and quarter of its columns: the parts' O and
-// sums, brought to the largest maximum, are added in the parts' order.
-constexpr int kJoinThreads = 256;
-constexpr int kMaxParts = kSms + 1;
+// A CTA per slot of a cut unit and 8 of its columns, a thread per row: the
+// parts' O and sums, brought to the largest maximum, are added in the parts'
+// order.
+constexpr int kJoinCols = 8;
 
 template <bool LSE>
-__global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const __grid_constant__ PrefixParams p, int n_cta) {
-    extern __shared__ float wgt[];                       // [parts][128] weights
-    const int slot = blockIdx.x >> 2, quarter = blockIdx.x & 3;
-    const int u = slot >> 1;
+__global__ void __launch_bounds__(kRows) prefix_join_kernel(const __grid_constant__ PrefixParams p, int n_cta) {
+    constexpr int kPer = kD / kJoinCols;
+    const int slot = blockIdx.x / kPer, q0 = (blockIdx.x % kPer) * (kJoinCols / 4);
+    const int u = slot >> 1, r = threadIdx.x;
     const long x = (long)u * n_cta, y = x + n_cta;
     const int c0 = (int)(x / p.U), n = (int)((y + p.U - 1) / p.U) - c0;      // the unit's parts
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (n <= 1) return;                                                     // written whole
+    const long orow = (long)slot * kRows + r;
+    if (n <= 1 || orow >= (long)p.R << p.hshift) return;                    // written whole; no such row
     const float* ws = p.ws + ((size_t)u * p.parts * 2 + (slot & 1)) * kPartFloats;
     const size_t stride = 2 * (size_t)kPartFloats;
-    const int r = threadIdx.x & 127, hi = threadIdx.x >> 7;
-    const long orow = (long)slot * kRows + r;
     float M = -INFINITY, lr = 0.0f, le = 0.0f;
+#pragma unroll 8
     for (int k = 0; k < n; ++k) M = fmaxf(M, ws[k * stride + kRows * kD + r]);
+    float4 a0 = make_float4(0.0f, 0.0f, 0.0f, 0.0f), a1 = a0;
+#pragma unroll 4
     for (int k = 0; k < n; ++k) {
-        const float* st = ws + k * stride + kRows * kD;
-        const float mk = st[r];
-        const float w = (mk == -INFINITY) ? 0.0f : exp2f(mk - M);
-        if (w != 0.0f) {
-            lr += w * st[kRows + r];
-            le += w * st[2 * kRows + r];
+        const float* part = ws + k * stride;
+        const float mk = part[kRows * kD + r];
+        const float l0 = part[kRows * kD + kRows + r], l1 = part[kRows * kD + 2 * kRows + r];
+        const float4 v0 = *reinterpret_cast<const float4*>(part + (q0 * kRows + r) * 4);
+        const float4 v1 = *reinterpret_cast<const float4*>(part + ((q0 + 1) * kRows + r) * 4);
+        if (mk > -INFINITY || mk != mk) {                // else no key: its O was not written
+            const float w = exp2f(mk - M);
+            lr += w * l0;
+            le += w * l1;
+            a0.x = fmaf(w, v0.x, a0.x);
+            a0.y = fmaf(w, v0.y, a0.y);
+            a0.z = fmaf(w, v0.z, a0.z);
+            a0.w = fmaf(w, v0.w, a0.w);
+            a1.x = fmaf(w, v1.x, a1.x);
+            a1.y = fmaf(w, v1.y, a1.y);
+            a1.z = fmaf(w, v1.z, a1.z);
+            a1.w = fmaf(w, v1.w, a1.w);
         }
-        if (hi == 0) wgt[k * kRows + r] = w;
     }
-    __syncthreads();
-    if (orow >= (long)p.R << p.hshift) return;
     const float inv = (lr == 0.0f) ? 0.0f : 1.0f / lr;
-    float4 acc[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) acc[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    const int q0 = quarter * 8 + hi * 4;                 // column quads q0 .. q0 + 3
-    for (int k = 0; k < n; ++k) {
-        const float w = wgt[k * kRows + r];
-        if (w == 0.0f) continue;                         // an empty part's O was not written
-        const float4* o = reinterpret_cast<const float4*>(ws + k * stride);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float4 v = o[(q0 + i) * kRows + r];
-            acc[i].x = fmaf(w, v.x, acc[i].x);
-            acc[i].y = fmaf(w, v.y, acc[i].y);
-            acc[i].z = fmaf(w, v.z, acc[i].z);
-            acc[i].w = fmaf(w, v.w, acc[i].w);
-        }
-    }
-    __nv_bfloat16* dst = p.out + orow * kD + q0 * 4;
-#pragma unroll
-    for (int i = 0; i < 4; i += 2) {
-        uint32_t w[4];
-        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[0]) : "f"(acc[i].y * inv), "f"(acc[i].x * inv));
-        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[1]) : "f"(acc[i].w * inv), "f"(acc[i].z * inv));
-        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[2]) : "f"(acc[i + 1].y * inv), "f"(acc[i + 1].x * inv));
-        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[3]) : "f"(acc[i + 1].w * inv), "f"(acc[i + 1].z * inv));
-        *reinterpret_cast<uint4*>(dst + i * 4) = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-    if (LSE && quarter == 0 && hi == 0) p.lse[orow] = (le == 0.0f) ? -INFINITY : (M + log2f(le)) / kLog2e;
+    uint32_t w[4];
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[0]) : "f"(a0.y * inv), "f"(a0.x * inv));
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[1]) : "f"(a0.w * inv), "f"(a0.z * inv));
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[2]) : "f"(a1.y * inv), "f"(a1.x * inv));
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[3]) : "f"(a1.w * inv), "f"(a1.z * inv));
+    *reinterpret_cast<uint4*>(p.out + orow * kD + q0 * 4) = make_uint4(w[0], w[1], w[2], w[3]);
+    if (LSE && q0 == 0) p.lse[orow] = (le == 0.0f) ? -INFINITY : (M + log2f(le)) / kLog2e;
 }
 
 // ---------------------------------------------------------------------- host
@@ -737,13 +758,13 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn_prefix() {
     return fn;
 }
 
-// 2D bf16 tensor [rows, 128] with a 128-byte-swizzled box of {64, 128}.
+// 2D bf16 tensor [rows, 128] with a 128-byte-swizzled box of {64, 64}.
 bool make_map_prefix(CUtensorMap* m, const void* ptr, uint64_t rows) {
     auto fn = encode_fn_prefix();
     if (!fn) return false;
     cuuint64_t dims[2] = {(cuuint64_t)kD, (cuuint64_t)rows};
     cuuint64_t strides[1] = {(cuuint64_t)kD * 2};
-    cuuint32_t box[2] = {64, (cuuint32_t)kBN};
+    cuuint32_t box[2] = {64, 64};
     cuuint32_t estr[2] = {1, 1};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box, estr,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -792,10 +813,14 @@ unsigned long long attention_prefix_tc_workspace(const AttnArgs& a) {
 
 cudaError_t launch_attention_prefix_tc(const AttnArgs& a, void* workspace, uint32_t* err, cudaStream_t s) {
     const Plan pl = plan_of(a);
-    CUtensorMap tm_q, tm_p;
-    if (!make_map_prefix(&tm_q, a.q, (uint64_t)pl.R * a.H)) return cudaErrorInvalidValue;
-    // (without prefix rows no shared tile is loaded: any valid address)
-    if (!make_map_prefix(&tm_p, a.N_p > 0 ? a.kv_p : a.q, a.N_p > 0 ? (uint64_t)a.N_p : 1)) return cudaErrorInvalidValue;
+    CUtensorMap tm_q, tm_p, tm_c, tm_w;
+    // (a tensor without rows is never loaded: any valid address)
+    const auto map = [&](CUtensorMap* m, const void* ptr, long n) {
+        return make_map_prefix(m, n > 0 ? ptr : a.q, n > 0 ? (uint64_t)n : 1);
+    };
+    if (!map(&tm_q, a.q, (long)pl.R * a.H) || !map(&tm_p, a.kv_p, a.N_p) || !map(&tm_c, a.kv_c, (long)a.B * a.N_cap) ||
+        !map(&tm_w, a.kv_raw, (long)a.B * a.L_raw))
+        return cudaErrorInvalidValue;
     PrefixParams p;
     p.kv_p = static_cast<const __nv_bfloat16*>(a.kv_p);
     p.kv_c = static_cast<const __nv_bfloat16*>(a.kv_c);
@@ -819,18 +844,14 @@ cudaError_t launch_attention_prefix_tc(const AttnArgs& a, void* workspace, uint3
                           : (lse ? attn_prefix_kernel<1, true> : attn_prefix_kernel<1, false>);
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
     if (e != cudaSuccess) return e;
-    kern<<<(unsigned)pl.n_cta, kThreads, kSmem, s>>>(tm_q, tm_p, p);
+    kern<<<(unsigned)pl.n_cta, kThreads, kSmem, s>>>(tm_q, tm_p, tm_c, tm_w, p);
     count_launch();
     e = cudaGetLastError();
     if (e != cudaSuccess || !cut) return e;
     auto join = lse ? prefix_join_kernel<true> : prefix_join_kernel<false>;
-    const size_t smem = (size_t)pl.parts * kRows * sizeof(float);
-    e = cudaFuncSetAttribute(join, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(kMaxParts * kRows * sizeof(float)));
-    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(pl.U * 2 * 4), 1, 1);
-    cfg.blockDim = dim3(kJoinThreads, 1, 1);
-    cfg.dynamicSmemBytes = smem;
+    cfg.gridDim = dim3((unsigned)(pl.U * 2 * (kD / kJoinCols)), 1, 1);
+    cfg.blockDim = dim3(kRows, 1, 1);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
