@@ -246,6 +246,14 @@ __device__ __forceinline__ float f2hi(uint64_t v) { return __uint_as_float((uint
 __device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
     asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
 }
+// True in one lane of a warp that is together (always the same one).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t on;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "elect.sync _|p, 0xffffffff;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(on));
+    return on != 0;
+}
 // 16-byte copy global -> shared, or 16 zero bytes (nothing is read) when !on.
 __device__ __forceinline__ void cp_async16_or_zero(void* dst, const void* src, bool on) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
@@ -403,96 +411,120 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         }
     } else if (warp == kMmaWarp) {
         // ------------------------------------------------------------ Q and every MMA
-        if (lane == 0) {
-            constexpr uint32_t id_qk = idesc_bf16(kRows, kBN, false, false);
-            constexpr uint32_t id_pv = idesc_bf16(kRows, kD, false, true);
-            const uint64_t qd0 = sw128_desc(smem_u32(sQ), 16, 1024), kd0 = sw128_desc(smem_u32(sK), 16, 1024);
-            const uint64_t vd0 = sw128_desc(smem_u32(sK), kHalf, 1024);
-            int ld0 = 0;                  // tiles of earlier units
-            uint32_t pp = 0;              // bit s: parity of slot s's next P
-            uint32_t po = 0;              // bit s: parity of slot s's next o_free (once it had a part)
-            uint32_t had = 0;             // bit s: slot s had tiles in an earlier part
-            int nq = 0, nfree = 0;        // Q loads; parts whose Q was used up
-            bool ok = true;
-            if (p.stall) mbar_wait(&ctl->stall_bar, 0, abort, p.err, p.wait_ns);
-            for (int u = u0; u < u1 && ok; ++u) {
-                const Geo g = geo[u - u0];
-                if (g.lo >= g.hi) continue;
-                if (*abort || (nfree > 0 && !wait_bar(&ctl->q_free, (nfree - 1) & 1, abort, p.err, p.wait_ns))) break;
+        // The whole warp runs this, kept together by votes, and elect.sync picks the
+        // issuing lane: for a branch on the lane number the compiler cannot know
+        // that one thread issues, and an MMA took 90 - 120 cycles to issue.
+        constexpr uint32_t id_qk = idesc_bf16(kRows, kBN, false, false);
+        constexpr uint32_t id_pv = idesc_bf16(kRows, kD, false, true);
+        const uint64_t qd0 = sw128_desc(smem_u32(sQ), 16, 1024), kd0 = sw128_desc(smem_u32(sK), 16, 1024);
+        const uint64_t vd0 = sw128_desc(smem_u32(sK), kHalf, 1024);
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+            return __all_sync(0xffffffffu, wait_bar(bar, parity, abort, p.err, p.wait_ns));
+        };
+        int ld0 = 0;                  // tiles of earlier units
+        uint32_t pp = 0;              // bit s: parity of slot s's next P
+        uint32_t po = 0;              // bit s: parity of slot s's next o_free (once it had a part)
+        uint32_t had = 0;             // bit s: slot s had tiles in an earlier part
+        int nq = 0, nfree = 0;        // Q loads; parts whose Q was used up
+        bool ok = true;
+        if (p.stall) ok = wait(&ctl->stall_bar, 0);
+        for (int u = u0; u < u1 && ok; ++u) {
+            Geo g = geo[u - u0];
+            g.P = __shfl_sync(0xffffffffu, g.P, 0);
+            g.T0 = __shfl_sync(0xffffffffu, g.T0, 0);
+            g.T1 = __shfl_sync(0xffffffffu, g.T1, 0);
+            g.on = __shfl_sync(0xffffffffu, g.on, 0);
+            g.lo = __shfl_sync(0xffffffffu, g.lo, 0);
+            g.hi = __shfl_sync(0xffffffffu, g.hi, 0);
+            if (g.lo >= g.hi) continue;
+            if (nfree > 0) ok = wait(&ctl->q_free, (nfree - 1) & 1);
+            ok = __all_sync(0xffffffffu, ok && *abort == 0);
+            if (!ok) break;
+            if (elect_one()) {
                 mbar_arrive_expect_tx(&ctl->bar_q, 2 * kTileBytes);
                 for (int k = 0; k < 8; ++k)
                     tma_load_2d(sQ + (k >> 1) * 8192 + (k & 1) * kHalf + (k >> 2) * kHalf, &tm_q, (k & 1) * 64,
                                 2 * u * kRows + (k >> 1) * 64, &ctl->bar_q);
-                ++nq;
-                ok = wait_bar(&ctl->bar_q, (nq - 1) & 1, abort, p.err, p.wait_ns);
-                // S of slot s = Q . tile `ld` of the CTA
-                auto issue_qk = [&](int s, int ld) -> bool {
-                    const int slot = ld % kStages;
-                    if (!wait_bar(&ctl->full[slot], (ld / kStages) & 1, abort, p.err, p.wait_ns)) return false;
-                    tc_fence_after();
-                    const uint64_t qd = qd0 + (uint64_t)(s * (kTileBytes >> 4)), kd = kd0 + (uint64_t)(slot * (kTileBytes >> 4));
+            }
+            __syncwarp();
+            ++nq;
+            ok = wait(&ctl->bar_q, (nq - 1) & 1);
+            // S of slot s = Q . tile `ld` of the CTA
+            auto issue_qk = [&](int s, int ld) -> bool {
+                const int slot = ld % kStages;
+                if (!wait(&ctl->full[slot], (ld / kStages) & 1)) return false;
+                tc_fence_after();
+                const uint64_t qd = qd0 + (uint64_t)(s * (kTileBytes >> 4)), kd = kd0 + (uint64_t)(slot * (kTileBytes >> 4));
+                if (elect_one()) {
 #pragma unroll
                     for (int kq = 0; kq < kD / 16; ++kq) {
                         const uint32_t off16 = ((kq >> 2) * kHalf + (kq & 3) * 32) >> 4;
-                        mma_bf16_ss(tmem + s * 128, qd + off16, kd + off16, id_qk, kq > 0);
+                        mma_bf16_ss(tm + s * 128, qd + off16, kd + off16, id_qk, kq > 0);
                     }
                     mma_commit(&ctl->s_full[s]);
-                    return true;
-                };
-                const int ldx = ld0 - g.lo;               // tile i of the list is the CTA's tile ldx + i
-                for (int s = 0; s < 2 && ok; ++s) {
-                    const int i = g.next_of(s, g.lo);
-                    if (i < g.hi) ok = issue_qk(s, ldx + i);
                 }
-                const int dual_end = g.on == 3 ? min(g.P, g.hi) : 0;    // tiles below it serve both slots
-                uint32_t first = 3u;
+                __syncwarp();
+                return true;
+            };
+            const int ldx = ld0 - g.lo;               // tile i of the list is the CTA's tile ldx + i
+            for (int s = 0; s < 2 && ok; ++s) {
+                const int i = g.next_of(s, g.lo);
+                if (i < g.hi) ok = issue_qk(s, ldx + i);
+            }
+            const int dual_end = g.on == 3 ? min(g.P, g.hi) : 0;    // tiles below it serve both slots
+            uint32_t first = 3u;
 #pragma unroll 1
-                for (int i = g.lo, s = 0; i < g.hi && ok;) {
-                    // slot s's P of tile i: O += P . V, then its next Q . K
-                    const int m = i < dual_end ? 3 : g.mask(i);
-                    const bool last = s == 1 || m == 1;   // the tile's last use
-                    if ((m >> s) & 1) {
-                        const int slot = (ldx + i) % kStages;
-                        const int nx = i + 1 < dual_end ? i + 1 : g.next_of(s, i + 1);
-                        ok = wait_bar(&ctl->p_ready[s], (pp >> s) & 1, abort, p.err, p.wait_ns);
-                        pp ^= 1u << s;
-                        if (ok && ((first & had) >> s & 1)) {          // the slot's previous O has been read
-                            ok = wait_bar(&ctl->o_free[s], (po >> s) & 1, abort, p.err, p.wait_ns);
-                            po ^= 1u << s;
-                        }
-                        if (!ok) break;
-                        tc_fence_after();
-                        const uint64_t vd = vd0 + (uint64_t)(slot * (kTileBytes >> 4));
-                        const uint32_t acc = ((first >> s) & 1) ^ 1u;
+            for (int i = g.lo, s = 0; i < g.hi && ok;) {
+                // slot s's P of tile i: O += P . V, then its next Q . K
+                const int m = i < dual_end ? 3 : g.mask(i);
+                const bool last = s == 1 || m == 1;   // the tile's last use
+                if ((m >> s) & 1) {
+                    const int slot = (ldx + i) % kStages;
+                    const int nx = i + 1 < dual_end ? i + 1 : g.next_of(s, i + 1);
+                    ok = wait(&ctl->p_ready[s], (pp >> s) & 1);
+                    pp ^= 1u << s;
+                    if (ok && ((first & had) >> s & 1)) {          // the slot's previous O has been read
+                        ok = wait(&ctl->o_free[s], (po >> s) & 1);
+                        po ^= 1u << s;
+                    }
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t vd = vd0 + (uint64_t)(slot * (kTileBytes >> 4));
+                    const uint32_t acc = ((first >> s) & 1) ^ 1u;
+                    if (elect_one()) {
 #pragma unroll
                         for (int kk = 0; kk < kBN / 16; ++kk)
-                            mma_bf16_ts(tmem + 256 + s * 128, tmem + s * 128 + (kk >> 2) * 64 + (kk & 3) * 8, vd + (uint64_t)(kk * (2048 >> 4)),
-                                        id_pv, kk > 0 ? 1u : acc);
-                        first &= ~(1u << s);
+                            mma_bf16_ts(tm + 256 + s * 128, tm + s * 128 + (kk >> 2) * 64 + (kk & 3) * 8,
+                                        vd + (uint64_t)(kk * (2048 >> 4)), id_pv, kk > 0 ? 1u : acc);
                         if (last) mma_commit(&ctl->freeb[slot]);
-                        if (nx < g.hi) {
-                            ok = issue_qk(s, ldx + nx);
-                        } else {
-                            mma_commit(&ctl->o_full[s]);
-                            had |= 1u << s;
-                        }
+                        if (nx >= g.hi) mma_commit(&ctl->o_full[s]);
                     }
-                    i += last;
-                    s = last ? 0 : 1;
+                    __syncwarp();
+                    first &= ~(1u << s);
+                    if (nx < g.hi) {
+                        ok = issue_qk(s, ldx + nx);
+                    } else {
+                        had |= 1u << s;
+                    }
                 }
-                if (ok) {
-                    mma_commit(&ctl->q_free);
-                    ++nfree;
-                }
-                ld0 += g.hi - g.lo;
+                i += last;
+                s = last ? 0 : 1;
             }
-            // every MMA must finish before TMEM is released, a Q load in
-            // flight must land before shared memory is given up
-            mma_commit(&ctl->fin);
-            volatile int never = 0;
-            mbar_wait(&ctl->fin, 0, &never, p.err);
-            if (nq > 0) mbar_wait(&ctl->bar_q, (nq - 1) & 1, &never, p.err);
+            if (ok) {
+                if (elect_one()) mma_commit(&ctl->q_free);
+                __syncwarp();
+                ++nfree;
+            }
+            ld0 += g.hi - g.lo;
         }
+        // every MMA must finish before TMEM is released, a Q load in flight
+        // must land before shared memory is given up
+        if (elect_one()) mma_commit(&ctl->fin);
+        __syncwarp();
+        volatile int never = 0;
+        mbar_wait(&ctl->fin, 0, &never, p.err);
+        if (nq > 0) mbar_wait(&ctl->bar_q, (nq - 1) & 1, &never, p.err);
         __syncwarp();
     } else {
         // ------------------------------------------------------------ softmax and output
