@@ -26,8 +26,7 @@
 // part [c U / G, (c+1) U / G) of the U units laid end to end, each unit's tiles
 // cut in that proportion.  A unit that stays whole is written out by its CTA;
 // the parts of a cut one leave their unnormalised O (fp32), running maximum
-// and sums in the workspace, and a second kernel, launched overlapped, joins
-// them in a fixed order.
+// and sums in the workspace, and a second kernel joins them in a fixed order.
 //
 // Roles (12 warps, one CTA per SM): warps 0-2 load key tiles; warp 3 allocates
 // TMEM and one lane loads Q (TMA) and issues every MMA; warps 4-7 / 8-11 run the
@@ -68,15 +67,18 @@ constexpr int kThreads = (kSoftWarp0 + 16) * 32;
 constexpr int kSms = 148;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescaleLog2 = 8.0f;
+constexpr float kRange = 0x1p40f;
 constexpr int kPartFloats = kRows * kD + 3 * kRows;    // O, then m, l_r, l_e of a slot's part
 
 struct __align__(8) Ctrl {
     uint64_t bar_q, q_free;
     uint64_t full[kStages], freeb[kStages];
     uint64_t s_full[2], p_ready[2], o_full[2], o_free[2];
+    uint64_t pair[2][4];                     // the two warps of a slot's 32 rows meet
     uint64_t fin, stall_bar;
     uint32_t tmem_base;
     int abort;
+    int redo[2];             // the slot's last P has a weight out of range: S is made again
     // between the two threads of a row: maximum, sums of rounded / exact weights
     float xm[2][2][kRows];
     float xl[2][2][2][2][kRows];             // (by unit parity)
@@ -91,7 +93,6 @@ struct PrefixParams {
     int R;                   // query rows
     int U;                   // units
     int parts;               // workspace slots per unit
-    int cut;                 // some unit is cut: a join follows
     float scale_log2;
     __nv_bfloat16* out;
     float* lse;
@@ -260,6 +261,27 @@ __device__ __forceinline__ void cp_async16_or_zero(void* dst, const void* src, b
                  ::"r"(smem_u32(dst)), "l"(src), "r"(on ? 16 : 0) : "memory");
 }
 
+// Largest of the first n (1 .. 64) S values at s_addr of this thread's row.
+__device__ __noinline__ float row_max(uint32_t s_addr, int n) {
+    float mx0 = -INFINITY, mx1 = -INFINITY;
+#pragma unroll 1
+    for (int c = 0; c < n; c += 32) {
+        float sv[32];
+        tmem_ld32(s_addr + c, sv);
+        if (n < c + 32) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+                if (c + e >= n) sv[e] = -INFINITY;
+        }
+#pragma unroll
+        for (int e = 0; e < 32; e += 4) {
+            mx0 = max3(mx0, sv[e], sv[e + 1]);
+            mx1 = max3(mx1, sv[e + 2], sv[e + 3]);
+        }
+    }
+    return fmaxf(mx0, mx1);
+}
+
 // The row maximum grew by more than 2^8: rescale this thread's half of the row's O.
 __device__ __noinline__ void rescale_o(uint32_t o_addr, float alpha) {
 #pragma unroll 1
@@ -304,6 +326,8 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             mbar_init(&ctl->o_full[i], 1);
             mbar_init(&ctl->o_free[i], 8);
         }
+        for (int i = 0; i < 8; ++i) mbar_init(&ctl->pair[i >> 2][i & 3], 2);
+        ctl->redo[0] = ctl->redo[1] = 0;
         mbar_init(&ctl->fin, 1);
         mbar_init(&ctl->stall_bar, 1);
         // a CTA started after another one timed out does no work
@@ -474,6 +498,7 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             }
             const int dual_end = g.on == 3 ? min(g.P, g.hi) : 0;    // tiles below it serve both slots
             uint32_t first = 3u;
+            uint32_t again = 0u;          // bit s: slot s makes its P again
 #pragma unroll 1
             for (int i = g.lo, s = 0; i < g.hi && ok;) {
                 // slot s's P of tile i: O += P . V, then its next Q . K
@@ -490,6 +515,18 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     }
                     if (!ok) break;
                     tc_fence_after();
+                    // a weight outgrew the range: S of this tile once more (the warps then
+                    // raise the maximum first); answered, the flag goes back
+                    if (__shfl_sync(0xffffffffu, *(volatile int*)&ctl->redo[s], 0)) {
+                        if (!((again >> s) & 1)) {
+                            again |= 1u << s;
+                            ok = issue_qk(s, ldx + i);
+                            continue;
+                        }
+                        again &= ~(1u << s);
+                        if (lane == 0) *(volatile int*)&ctl->redo[s] = 0;
+                        __syncwarp();
+                    }
                     const uint64_t vd = vd0 + (uint64_t)(slot * (kTileBytes >> 4));
                     const uint32_t acc = ((first >> s) & 1) ^ 1u;
                     if (elect_one()) {
@@ -535,19 +572,16 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         const uint32_t s_addr = tmem + lane_addr + s * 128;
         const uint32_t o_addr = tmem + lane_addr + 256 + s * 128 + 64 * h;
         const int grp = r / H;                               // the row's query row in the slot
-        // The row's two warps meet here once per tile; the result is the OR of
-        // both warps' flags.  A warp whose wait ran out comes too, so neither is
-        // left waiting; the abort flag is set before it comes.
-        const int pair_id = 1 + s * 4 + (warp & 3);
-        auto pair_or = [&](bool flag) -> bool {
-            uint32_t any;
-            asm volatile("{\n\t.reg .pred q, r;\n\t"
-                         "setp.ne.u32 q, %1, 0;\n\t"
-                         "barrier.cta.red.or.pred r, %2, 64, q;\n\t"
-                         "selp.u32 %0, 1, 0, r;\n\t}"
-                         : "=r"(any) : "r"((uint32_t)flag), "r"(pair_id) : "memory");
-            return any != 0;
+        // The row's two warps meet (a bounded wait).
+        uint32_t px = 0;
+        auto pair_sync = [&]() -> bool {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl->pair[s][warp & 3]);
+            const bool o = __all_sync(0xffffffffu, wait_bar(&ctl->pair[s][warp & 3], px, abort, p.err, p.wait_ns));
+            px ^= 1;
+            return o;
         };
+        volatile int* redo = &ctl->redo[s];
         uint32_t ps = 0, po = 0;                             // parities of s_full, o_full
         bool ok = true;
         for (int u = u0; u < u1 && ok; ++u) {
@@ -555,72 +589,82 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             const int qrow = (2 * u + s) * G + grp;
             const RowRec row = rows[((u - u0) * 2 + s) * G + grp];
             const int own_len = row.n_pre + row.n_own + row.n_win;
-            float m_used = -INFINITY, l_r = 0.0f, l_e = 0.0f;
+            // m_used: the maximum in use (base 2); l_r, l_e: this half's sums of the
+            // rounded / exact weights, l_r0, l_e0 those before the last tile
+            float m_used = -INFINITY, l_r = 0.0f, l_e = 0.0f, l_r0 = 0.0f, l_e0 = 0.0f;
             int n = 0;                                       // tiles of this part
+            int nv = 0;
 #pragma unroll 1
-            for (int i = g.lo; i < g.hi; ++i) {
-                if (!((g.mask(i) >> s) & 1)) continue;
+            for (int i = g.next_of(s, g.lo); i < g.hi;) {
+                // (what the tile needs is worked out before the wait for it)
                 // this half's columns that are keys of the row (the same in all lanes)
-                int nv = 64;
+                int nvi = 64;
                 if (i >= g.P) {
-                    nv = own_len - g.own_step(i) * H - (G == 1 ? 64 * h : 0);
-                    nv = (G == 2 && h != grp) ? 0 : max(min(nv, 64), 0);
+                    nvi = own_len - g.own_step(i) * H - (G == 1 ? 64 * h : 0);
+                    nvi = (G == 2 && h != grp) ? 0 : max(min(nvi, 64), 0);
                 }
+                int nx = g.next_of(s, i + 1);
                 // every wait is warp-collective: the TMEM accesses below are .sync.aligned
                 ok = __all_sync(0xffffffffu, wait_bar(&ctl->s_full[s], ps, abort, p.err, p.wait_ns));
+                if (!ok) break;
                 ps ^= 1;
                 tc_fence_after();
-                if (!ok) {
-                    pair_or(true);
-                    break;
+                const bool back = *redo != 0;                // the tile before, again
+                if (back) {
+                    nx = i;
+                    l_r = l_r0;
+                    l_e = l_e0;
+                } else {
+                    nv = nvi;
+                    l_r0 = l_r;
+                    l_e0 = l_e;
                 }
-                float sv[64];
-                for (bool again = false;; again = true) {
-                    tmem_ld64(s_addr + 64 * h, sv);
-                    if (nv < 64) {
-#pragma unroll
-                        for (int e = 0; e < 64; ++e)
-                            if (e >= nv) sv[e] = -INFINITY;
-                    }
-                    float mx = -INFINITY, mx1 = -INFINITY;
-#pragma unroll
-                    for (int e = 0; e < 64; e += 4) {
-                        mx = max3(mx, sv[e], sv[e + 1]);
-                        mx1 = max3(mx1, sv[e + 2], sv[e + 3]);
-                    }
-                    mx = fmaxf(mx, mx1) * p.scale_log2;
-                    // the maximum in use is raised (and O rescaled) where a score outgrows
-                    // it by more than 2^8; true for a row's first keys
-                    if (again || !pair_or(mx > m_used + kRescaleLog2)) break;
-                    ok = *abort == 0;
-                    if (!ok) break;
+                // The maximum of the part's first tile serves the later ones: bf16 and
+                // fp32 hold weights up to kRange times it without loss.  A tile with
+                // larger ones is made again with the maximum raised first; the last
+                // tile, after which S is not made any more, looks for it beforehand.
+                const bool seek = back || n == 0 || nx >= g.hi;
+                if (seek) {
+                    float mx = -INFINITY;
+                    if (nv > 0) mx = row_max(s_addr + 64 * h, nv) * p.scale_log2;
                     ctl->xm[s][h][r] = mx;
-                    pair_or(false);
+                    ok = pair_sync();
+                    if (!ok) break;
+                    // (xm is written again only after the next s_full, which both warps'
+                    // p_ready precede)
                     mx = fmaxf(mx, ctl->xm[s][h ^ 1][r]);
                     float alpha = 1.0f;
-                    if (mx > m_used + kRescaleLog2) {
+                    const bool raise = mx > m_used + kRescaleLog2;       // true for a row's first keys
+                    if (raise) {
                         alpha = (m_used == -INFINITY) ? 0.0f : ex2(m_used - mx);
                         m_used = mx;
                         l_r *= alpha;
                         l_e *= alpha;
                     }
                     // (s_full of this tile was committed after the P.V of the one
-                    // before was issued, so that P.V has completed: O is stable.)
-                    // S is read again rather than kept in registers across the call.
-                    if (n > 0) rescale_o(o_addr, alpha);
+                    // before was issued, so that P.V has completed: O is stable)
+                    if (n > 0 && __any_sync(0xffffffffu, raise)) rescale_o(o_addr, alpha);
                 }
-                if (!ok) break;
                 // P of this half's 64 keys, over the S it was made from
+                bool large = false;
                 if (nv > 0) {
                     const float mm = (m_used == -INFINITY) ? 0.0f : m_used;
                     const uint64_t sl2 = f2_pack(p.scale_log2, p.scale_log2), negm = f2_pack(-mm, -mm);
                     uint64_t accr = 0, acce = 0;
-#pragma unroll
+                    // (rolled: this much straight-line code would wait for its instructions)
+#pragma unroll 1
                     for (int q = 0; q < 2; ++q) {
+                        float sv[32];
+                        tmem_ld32(s_addr + 64 * h + 32 * q, sv);
+                        if (nv < 64) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if (32 * q + e >= nv) sv[e] = -INFINITY;
+                        }
                         uint32_t pk[16];
 #pragma unroll
                         for (int e = 0; e < 32; e += 2) {
-                            const uint64_t z = f2_fma(f2_pack(sv[32 * q + e], sv[32 * q + e + 1]), sl2, negm);
+                            const uint64_t z = f2_fma(f2_pack(sv[e], sv[e + 1]), sl2, negm);
                             const float p0 = ex2(f2lo(z)), p1 = ex2(f2hi(z));
                             uint32_t d;
                             asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(p1), "f"(p0));
@@ -630,7 +674,9 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         }
                         tmem_st16(s_addr + 64 * h + 16 * q, pk);
                     }
-                    l_r += f2lo(accr) + f2hi(accr);
+                    const float sum = f2lo(accr) + f2hi(accr);
+                    large = !(sum < kRange) || m_used == -INFINITY;      // (no maximum yet: the row's first keys)
+                    l_r += sum;
                     l_e += f2lo(acce) + f2hi(acce);
                 } else {
                     uint32_t zero[16];
@@ -639,11 +685,16 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     tmem_st16(s_addr + 64 * h, zero);
                     tmem_st16(s_addr + 64 * h + 16, zero);
                 }
+                if (!seek && __any_sync(0xffffffffu, large)) {
+                    if (lane == 0) *redo = 1;
+                    __threadfence_block();
+                }
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ctl->p_ready[s]);
-                ++n;
+                n += !back;
+                i = nx;
             }
             if (!ok) break;
             // ---------------------------------------------------------- the part's end
@@ -654,7 +705,8 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             }
             ctl->xl[u & 1][s][h][0][r] = l_r;
             ctl->xl[u & 1][s][h][1][r] = l_e;
-            if (pair_or(!ok)) { ok = false; break; }
+            ok = ok && pair_sync();
+            if (!ok) break;
             l_r += ctl->xl[u & 1][s][h ^ 1][0][r];
             l_e += ctl->xl[u & 1][s][h ^ 1][1][r];
             const long orow = (long)(2 * u + s) * kRows + r;         // flattened (row, head)
@@ -714,8 +766,6 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             }
         }
     }
-    // the join may start its launch; it waits for this grid's end before it reads
-    if (p.cut) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // (the MMA issuer waited for its final commit: no MMA is in flight)
     tc_fence_before();
     __syncthreads();
@@ -724,56 +774,113 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 }
 
 // ---------------------------------------------------------------------- join
-// A CTA per slot of a cut unit and 8 of its columns, a thread per row: the
-// parts' O and sums, brought to the largest maximum, are added in the parts'
-// order.
+// A CTA per slot of a cut unit and 8 of its columns; a thread per row and
+// quarter of the parts.  What bounds it is the latency of the loads (a few
+// parts of L2-resident data), so a thread's parts are fetched at once, 5 at a
+// time (a unit is cut into about 10 parts or, alone on the GPU, 20), and the
+// four partial results meet in shared memory.  The order of the sums is fixed.
 constexpr int kJoinCols = 8;
+constexpr int kJoinGroups = 4;
+constexpr int kJoinBatch = 5;
+
+struct JoinState {
+    float m, lr, le;
+    float o[kJoinCols];
+    // brings this state's scale to maximum M (its own is not above it)
+    __device__ __forceinline__ void rescale(float M) {
+        const float w = (m == -INFINITY) ? 0.0f : exp2f(m - M);
+        m = M;
+        lr *= w;
+        le *= w;
+#pragma unroll
+        for (int i = 0; i < kJoinCols; ++i) o[i] *= w;
+    }
+};
 
 template <bool LSE>
-__global__ void __launch_bounds__(kRows) prefix_join_kernel(const __grid_constant__ PrefixParams p, int n_cta) {
+__global__ void __launch_bounds__(kJoinGroups * kRows)
+prefix_join_kernel(const __grid_constant__ PrefixParams p, int n_cta) {
     constexpr int kPer = kD / kJoinCols;
+    __shared__ float sh[kJoinGroups - 1][3 + kJoinCols][kRows];
     const int slot = blockIdx.x / kPer, q0 = (blockIdx.x % kPer) * (kJoinCols / 4);
-    const int u = slot >> 1, r = threadIdx.x;
+    const int u = slot >> 1, r = threadIdx.x & (kRows - 1), grp = threadIdx.x / kRows;
     const long x = (long)u * n_cta, y = x + n_cta;
     const int c0 = (int)(x / p.U), n = (int)((y + p.U - 1) / p.U) - c0;      // the unit's parts
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (n <= 1) return;                                                     // written whole
     const long orow = (long)slot * kRows + r;
-    if (n <= 1 || orow >= (long)p.R << p.hshift) return;                    // written whole; no such row
     const float* ws = p.ws + ((size_t)u * p.parts * 2 + (slot & 1)) * kPartFloats;
     const size_t stride = 2 * (size_t)kPartFloats;
-    float M = -INFINITY, lr = 0.0f, le = 0.0f;
-#pragma unroll 8
-    for (int k = 0; k < n; ++k) M = fmaxf(M, ws[k * stride + kRows * kD + r]);
-    float4 a0 = make_float4(0.0f, 0.0f, 0.0f, 0.0f), a1 = a0;
-#pragma unroll 4
-    for (int k = 0; k < n; ++k) {
-        const float* part = ws + k * stride;
-        const float mk = part[kRows * kD + r];
-        const float l0 = part[kRows * kD + kRows + r], l1 = part[kRows * kD + 2 * kRows + r];
-        const float4 v0 = *reinterpret_cast<const float4*>(part + (q0 * kRows + r) * 4);
-        const float4 v1 = *reinterpret_cast<const float4*>(part + ((q0 + 1) * kRows + r) * 4);
-        if (mk > -INFINITY || mk != mk) {                // else no key: its O was not written
-            const float w = exp2f(mk - M);
-            lr += w * l0;
-            le += w * l1;
-            a0.x = fmaf(w, v0.x, a0.x);
-            a0.y = fmaf(w, v0.y, a0.y);
-            a0.z = fmaf(w, v0.z, a0.z);
-            a0.w = fmaf(w, v0.w, a0.w);
-            a1.x = fmaf(w, v1.x, a1.x);
-            a1.y = fmaf(w, v1.y, a1.y);
-            a1.z = fmaf(w, v1.z, a1.z);
-            a1.w = fmaf(w, v1.w, a1.w);
+    JoinState t;
+    t.m = -INFINITY;
+    t.lr = t.le = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kJoinCols; ++i) t.o[i] = 0.0f;
+    for (int k0 = grp; k0 < n; k0 += kJoinGroups * kJoinBatch) {
+        float m[kJoinBatch], lr[kJoinBatch], le[kJoinBatch];
+        float4 v0[kJoinBatch], v1[kJoinBatch];
+        float M = t.m;
+#pragma unroll
+        for (int j = 0; j < kJoinBatch; ++j) {
+            const int k = min(k0 + j * kJoinGroups, n - 1);
+            const float* part = ws + k * stride;
+            m[j] = part[kRows * kD + r];
+            lr[j] = part[kRows * kD + kRows + r];
+            le[j] = part[kRows * kD + 2 * kRows + r];
+            v0[j] = *reinterpret_cast<const float4*>(part + (q0 * kRows + r) * 4);
+            v1[j] = *reinterpret_cast<const float4*>(part + ((q0 + 1) * kRows + r) * 4);
+        }
+#pragma unroll
+        for (int j = 0; j < kJoinBatch; ++j)
+            if (k0 + j * kJoinGroups < n) M = fmaxf(M, m[j]);
+        t.rescale(M);
+#pragma unroll
+        for (int j = 0; j < kJoinBatch; ++j) {
+            // a part without keys of the row (m = -inf) left nothing to read in O
+            if (k0 + j * kJoinGroups >= n || m[j] == -INFINITY) continue;
+            const float w = exp2f(m[j] - M);
+            t.lr += w * lr[j];
+            t.le += w * le[j];
+            t.o[0] = fmaf(w, v0[j].x, t.o[0]);
+            t.o[1] = fmaf(w, v0[j].y, t.o[1]);
+            t.o[2] = fmaf(w, v0[j].z, t.o[2]);
+            t.o[3] = fmaf(w, v0[j].w, t.o[3]);
+            t.o[4] = fmaf(w, v1[j].x, t.o[4]);
+            t.o[5] = fmaf(w, v1[j].y, t.o[5]);
+            t.o[6] = fmaf(w, v1[j].z, t.o[6]);
+            t.o[7] = fmaf(w, v1[j].w, t.o[7]);
         }
     }
-    const float inv = (lr == 0.0f) ? 0.0f : 1.0f / lr;
+    if (grp > 0) {
+        float(*d)[kRows] = sh[grp - 1];
+        d[0][r] = t.m;
+        d[1][r] = t.lr;
+        d[2][r] = t.le;
+#pragma unroll
+        for (int i = 0; i < kJoinCols; ++i) d[3 + i][r] = t.o[i];
+    }
+    __syncthreads();
+    if (grp > 0 || orow >= (long)p.R << p.hshift) return;
+    float M = t.m;
+#pragma unroll
+    for (int j = 0; j < kJoinGroups - 1; ++j) M = fmaxf(M, sh[j][0][r]);
+    t.rescale(M);
+#pragma unroll
+    for (int j = 0; j < kJoinGroups - 1; ++j) {
+        const float mk = sh[j][0][r];
+        if (mk == -INFINITY) continue;
+        const float w = exp2f(mk - M);
+        t.lr += w * sh[j][1][r];
+        t.le += w * sh[j][2][r];
+#pragma unroll
+        for (int i = 0; i < kJoinCols; ++i) t.o[i] = fmaf(w, sh[j][3 + i][r], t.o[i]);
+    }
+    const float inv = (t.lr == 0.0f) ? 0.0f : 1.0f / t.lr;
     uint32_t w[4];
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[0]) : "f"(a0.y * inv), "f"(a0.x * inv));
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[1]) : "f"(a0.w * inv), "f"(a0.z * inv));
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[2]) : "f"(a1.y * inv), "f"(a1.x * inv));
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[3]) : "f"(a1.w * inv), "f"(a1.z * inv));
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(t.o[2 * i + 1] * inv), "f"(t.o[2 * i] * inv));
     *reinterpret_cast<uint4*>(p.out + orow * kD + q0 * 4) = make_uint4(w[0], w[1], w[2], w[3]);
-    if (LSE && q0 == 0) p.lse[orow] = (le == 0.0f) ? -INFINITY : (M + log2f(le)) / kLog2e;
+    if (LSE && q0 == 0) p.lse[orow] = (t.le == 0.0f) ? -INFINITY : (M + log2f(t.le)) / kLog2e;
 }
 
 // ---------------------------------------------------------------------- host
@@ -870,7 +977,6 @@ cudaError_t launch_attention_prefix_tc(const AttnArgs& a, void* workspace, uint3
     p.wait_ns = wait_limit_ns();
     p.stall = take_stall();
     const bool cut = attention_prefix_tc_workspace(a) > 0;
-    p.cut = cut;
     const bool lse = a.lse_out != nullptr;
     auto kern = a.H == 64 ? (lse ? attn_prefix_kernel<2, true> : attn_prefix_kernel<2, false>)
                           : (lse ? attn_prefix_kernel<1, true> : attn_prefix_kernel<1, false>);
@@ -881,18 +987,10 @@ cudaError_t launch_attention_prefix_tc(const AttnArgs& a, void* workspace, uint3
     e = cudaGetLastError();
     if (e != cudaSuccess || !cut) return e;
     auto join = lse ? prefix_join_kernel<true> : prefix_join_kernel<false>;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(pl.U * 2 * (kD / kJoinCols)), 1, 1);
-    cfg.blockDim = dim3(kRows, 1, 1);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, join, p, pl.n_cta);
+    // (launched in stream order: started early, its waiting CTAs cost the call 6 us)
+    join<<<(unsigned)(pl.U * 2 * (kD / kJoinCols)), kJoinGroups * kRows, 0, s>>>(p, pl.n_cta);
     count_launch();
-    return e != cudaSuccess ? e : cudaGetLastError();
+    return cudaGetLastError();
 }
 
 }  // namespace csa
