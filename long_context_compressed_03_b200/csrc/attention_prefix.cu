@@ -34,10 +34,11 @@
 // (Two M tiles a CTA, each with one S, shared the key tiles but ran S -> P -> S
 // as a chain: 1.4 times the time a tile, and twice the O to join.)
 //
-// The maximum.  The weights are exp2(z - m) with m the row's maximum over the
-// part's first tile: fp32 sums and bf16 weights lose nothing while z - m stays
-// below 64, so no running maximum is kept.  Where a sum of weights reaches
-// 2^64, the part is run again: once for the maxima alone, once with them.
+// The offset.  The weights are exp2(z - m) with m the row's score of one key of
+// the part's first tile, not a maximum: the true maximum is not below it, so
+// nothing that counts underflows, and fp32 sums and bf16 weights lose nothing
+// while z - m stays below 64.  Where a sum of weights reaches 2^64, the part is
+// run again: once for the rows' maxima alone, once with those as m.
 // P has bf16's 8 significant bits (A and B of an MMA share their type, and the
 // keys are bf16): its rounding moves an output by at most 2^-8 of the spread of
 // the averaged values, like the rounding of the output itself.  The output
@@ -83,15 +84,14 @@ struct __align__(8) Ctrl {
     uint64_t full[kStages], freeb[kStages];
     uint64_t s_full[kBufs], p_ready[kBufs], s_free[kBufs];
     uint64_t o_full, o_free;
-    uint64_t pair[2][4];     // the two warps of a group's 32 rows meet
-    uint64_t m_ready;        // the first tile's group has the rows' maxima
+    uint64_t m_ready;        // the rows' offsets are there
     uint64_t done;           // every warp is through with the attempt
     uint64_t fin[2], stall_bar;
     uint32_t tmem_base;
     int abort;
     int q_ahead;             // the first unit's Q was requested in the prologue
     int over[3];             // (attempt mod 3) some sum of weights left the range
-    float m[kRows];          // maxima in use (base 2)
+    float m[kRows];          // offsets in use (base 2)
     float xm[4][kRows];      // per thread of a row: its maximum
     float xl[2][4][2][kRows];   // (by attempt parity) its sums of rounded / exact weights
 };
@@ -131,6 +131,15 @@ struct Geo {
 };
 constexpr size_t kSmem = 1024 + kTileBytes + kStages * kTileBytes + sizeof(Ctrl) +
                          kMaxUnits * (sizeof(Geo) + 2 * sizeof(RowRec));
+
+// x / n for x >= 0 (64-bit division only where it is needed).
+__device__ __forceinline__ int div_of(long x, int n) {
+    return x < (1L << 31) ? (int)((unsigned)x / (unsigned)n) : (int)(x / n);
+}
+__device__ __forceinline__ int first_unit(const PrefixParams& p, int c, int n) { return div_of((long)c * p.U, n); }
+__device__ __forceinline__ int end_unit(const PrefixParams& p, int c, int n) {
+    return div_of((long)(c + 1) * p.U + n - 1, n);
+}
 
 // The CTA's units u0 .. u0 + n - 1: a thread per query row, then one per unit.
 template <int G>
@@ -174,18 +183,13 @@ __device__ __forceinline__ void fill_geometry(const PrefixParams& p, int c, int 
         }
         // CTA c takes [c U, (c+1) U) of the line on which unit u is [u n_cta, (u+1) n_cta)
         const long a = (long)c * p.U, b = a + p.U, x = (long)(u0 + k) * n_cta, y = x + n_cta;
-        g.lo = (int)((max(a, x) - x) * (g.P + g.T) / n_cta);
-        g.hi = (int)((min(b, y) - x) * (g.P + g.T) / n_cta);
-        g.ord = c - (int)(x / p.U);
+        g.lo = div_of((max(a, x) - x) * (g.P + g.T), n_cta);
+        g.hi = div_of((min(b, y) - x) * (g.P + g.T), n_cta);
+        g.ord = c - div_of(x, p.U);
         g.whole = a <= x && b >= y;
         geo[k] = g;
     }
 }
-__device__ __forceinline__ int first_unit(const PrefixParams& p, int c, int n) { return (int)((long)c * p.U / n); }
-__device__ __forceinline__ int end_unit(const PrefixParams& p, int c, int n) {
-    return (int)(((long)(c + 1) * p.U + n - 1) / n);
-}
-
 // A bounded wait: one try in line, the rest out of line.
 __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* err,
                                        uint64_t limit_ns) {
@@ -240,6 +244,13 @@ __device__ __forceinline__ void cp_async16_or_zero(void* dst, const void* src, b
                  ::"r"(smem_u32(dst)), "l"(src), "r"(on ? 16 : 0) : "memory");
 }
 
+// One fp32 column of this thread's TMEM lane.
+__device__ __forceinline__ float tmem_ld1(uint32_t taddr) {
+    uint32_t v;
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\t"
+                 "tcgen05.wait::ld.sync.aligned;" : "=r"(v) : "r"(taddr) : "memory");
+    return __uint_as_float(v);
+}
 // Largest of the first n (1 .. 64) S values at s_addr of this thread's row.
 __device__ __noinline__ float row_max(uint32_t s_addr, int n) {
     float mx0 = -INFINITY, mx1 = -INFINITY;
@@ -304,8 +315,7 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         }
         mbar_init(&ctl->o_full, 1);
         mbar_init(&ctl->o_free, kSoftWarps);
-        for (int i = 0; i < 8; ++i) mbar_init(&ctl->pair[i >> 2][i & 3], 2);
-        mbar_init(&ctl->m_ready, kSoftWarps / 2);
+        mbar_init(&ctl->m_ready, 4);
         mbar_init(&ctl->done, kThreads / 32);
         for (int i = 0; i < 2; ++i) mbar_init(&ctl->fin[i], 1);
         mbar_init(&ctl->stall_bar, 1);
@@ -398,17 +408,17 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                                 }
                                 continue;
                             }
-                            // row by row, zero rows past the list's end
+                            // row by row, zero rows past the list's end (nothing is read there)
                             copies = true;
-#pragma unroll 1
-                            for (int rr = lt >> 4; rr < 64; rr += kLoadThreads / 16) {
-                                const int jj = j + rr;
-                                const __nv_bfloat16* src = p.out;      // any address: nothing is read past the end
-                                if (jj < e1) src = p.kv_raw + ((size_t)rw.b * p.a.L_raw + rw.win_lo + jj) * kD;
-                                else if (jj < e2) src = p.kv_p + (size_t)(g.P * kBN + (jj - e1)) * kD;
-                                else if (jj < e3) src = p.kv_c + ((size_t)rw.b * p.a.N_cap + (jj - e2)) * kD;
-                                cp_async16_or_zero(dst + col + (64 * q + rr) * 128 + (((c16 & 7) ^ (rr & 7)) << 4), src + c16 * 8,
-                                                   jj < e3);
+                            const __nv_bfloat16* pw = p.kv_raw + ((long)rw.b * p.a.L_raw + rw.win_lo + j) * kD + c16 * 8;
+                            const __nv_bfloat16* pp = p.kv_p + ((long)g.P * kBN + j - e1) * kD + c16 * 8;
+                            const __nv_bfloat16* po = p.kv_c + ((long)rw.b * p.a.N_cap + j - e2) * kD + c16 * 8;
+#pragma unroll 4
+                            for (int it = 0; it < 64 / (kLoadThreads / 16); ++it) {
+                                const int rr = (lt >> 4) + it * (kLoadThreads / 16), jj = j + rr;
+                                const __nv_bfloat16* src = jj < e1 ? pw : (jj < e2 ? pp : po);
+                                src = jj < e3 ? src + rr * kD : p.out;
+                                cp_async16_or_zero(dst + col + (64 * q + rr) * 128 + (((c16 & 7) ^ (rr & 7)) << 4), src, jj < e3);
                             }
                         }
                     }
@@ -548,7 +558,6 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         const int r = (warp & 3) * 32 + lane;                // row of the unit
         const uint32_t my = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const int grp = r / H;                               // its query row in the unit
-        uint32_t px = 0;                                     // parity of pair
         int L = 0, L_grp = gr;                               // tiles so far; this group's next
         int no = 0, nm = 0;                                  // O's made; first tiles met
         bool ok = true;
@@ -563,7 +572,7 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 l_r = l_e = 0.0f;
                 m = mode == kExact ? ctl->m[r] : -INFINITY;
                 const bool leads = L_grp == L;               // this group has the attempt's first tile
-                bool have_m = mode != kFast;
+                bool have_m = mode != kFast;                 // kFast: m comes with the first tile
                 float top = -INFINITY;                       // kMax: largest score seen
                 bool large = false;
 #pragma unroll 1
@@ -584,25 +593,21 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         if (nv > 0) top = fmaxf(top, row_max(s_addr, nv));
                     } else {
                         if (!have_m) {
-                            // the rows' maxima over the part's first tile, from the group that
-                            // has it.  (A row without keys there has none in the part: the
-                            // lists are filled from the front.)
-                            if (leads) {
-                                ctl->xm[id][r] = nv > 0 ? row_max(s_addr, nv) * p.scale_log2 : -INFINITY;
-                                __syncwarp();
-                                if (lane == 0) mbar_arrive(&ctl->pair[gr][warp & 3]);
-                                ok = wait(&ctl->pair[gr][warp & 3], px);
-                                px ^= 1;
-                                if (!ok) break;
-                                m = fmaxf(ctl->xm[id][r], ctl->xm[id ^ 1][r]);
-                                if (h == 0) ctl->m[r] = m;
+                            // the row's first score in the first tile, from the group that has
+                            // it.  (A row without keys there has none in the part: the lists
+                            // are filled from the front.)
+                            if (leads && h == 0) {
+                                const int c0 = i < g.P ? 0 : grp * H;
+                                float z = tmem_ld1(my + buf * 128 + c0) * p.scale_log2;
+                                if (!(fabsf(z) < INFINITY)) z = 0.0f;
+                                if (i >= g.P && own_len <= (i - g.P) * H) z = -INFINITY;
+                                ctl->m[r] = z;
                                 __syncwarp();
                                 if (lane == 0) mbar_arrive(&ctl->m_ready);
-                            } else {
-                                ok = wait(&ctl->m_ready, nm & 1);
-                                if (!ok) break;
-                                m = ctl->m[r];
                             }
+                            ok = wait(&ctl->m_ready, nm & 1);
+                            if (!ok) break;
+                            m = ctl->m[r];
                             have_m = true;
                         }
                         // P of this half's 64 keys, over the S it is made from
