@@ -739,14 +739,12 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 }
 
 // ---------------------------------------------------------------------- join
-// A CTA per cut unit and 8 of its columns; a thread per row and
-// quarter of the parts.  What bounds it is the latency of the loads (a few
-// parts of L2-resident data), so a thread's parts are fetched at once, 5 at a
-// time (a unit is cut into about 10 parts or, alone on the GPU, 20), and the
-// four partial results meet in shared memory.  The order of the sums is fixed.
+// A CTA per cut unit and 8 of its columns; a thread per row and share of the
+// parts.  What bounds it is the latency of the loads (a few parts of
+// L2-resident data): a thread's parts are fetched kBatch at a time, and where a
+// unit has many parts (few units, so few CTAs), kGroups threads share a row and
+// meet in shared memory.  The order of the sums is fixed.
 constexpr int kJoinCols = 8;
-constexpr int kJoinGroups = 4;
-constexpr int kJoinBatch = 5;
 
 struct JoinState {
     float m, lr, le;
@@ -762,11 +760,11 @@ struct JoinState {
     }
 };
 
-template <bool LSE>
-__global__ void __launch_bounds__(kJoinGroups * kRows)
+template <bool LSE, int kGroups, int kBatch>
+__global__ void __launch_bounds__(kGroups * kRows)
 prefix_join_kernel(const __grid_constant__ PrefixParams p, int n_cta) {
     constexpr int kPer = kD / kJoinCols;
-    __shared__ float sh[kJoinGroups - 1][3 + kJoinCols][kRows];
+    __shared__ float sh[kGroups > 1 ? kGroups - 1 : 1][3 + kJoinCols][kRows];
     const int u = blockIdx.x / kPer, q0 = (blockIdx.x % kPer) * (kJoinCols / 4);
     const int r = threadIdx.x & (kRows - 1), grp = threadIdx.x / kRows;
     const long x = (long)u * n_cta, y = x + n_cta;
@@ -780,13 +778,15 @@ prefix_join_kernel(const __grid_constant__ PrefixParams p, int n_cta) {
     t.lr = t.le = 0.0f;
 #pragma unroll
     for (int i = 0; i < kJoinCols; ++i) t.o[i] = 0.0f;
-    for (int k0 = grp; k0 < n; k0 += kJoinGroups * kJoinBatch) {
-        float m[kJoinBatch], lr[kJoinBatch], le[kJoinBatch];
-        float4 v0[kJoinBatch], v1[kJoinBatch];
+    for (int k0 = grp; k0 < n; k0 += kGroups * kBatch) {
+        float m[kBatch], lr[kBatch], le[kBatch];
+        float4 v0[kBatch], v1[kBatch];
         float M = t.m;
 #pragma unroll
-        for (int j = 0; j < kJoinBatch; ++j) {
-            const int k = min(k0 + j * kJoinGroups, n - 1);
+        for (int j = 0; j < kBatch; ++j) {
+            const int k = k0 + j * kGroups;
+            m[j] = -INFINITY;
+            if (k >= n) continue;
             const float* part = ws + k * stride;
             m[j] = part[kRows * kD + r];
             lr[j] = part[kRows * kD + kRows + r];
@@ -795,13 +795,13 @@ prefix_join_kernel(const __grid_constant__ PrefixParams p, int n_cta) {
             v1[j] = *reinterpret_cast<const float4*>(part + ((q0 + 1) * kRows + r) * 4);
         }
 #pragma unroll
-        for (int j = 0; j < kJoinBatch; ++j)
-            if (k0 + j * kJoinGroups < n) M = fmaxf(M, m[j]);
+        for (int j = 0; j < kBatch; ++j)
+            M = fmaxf(M, m[j]);
         t.rescale(M);
 #pragma unroll
-        for (int j = 0; j < kJoinBatch; ++j) {
+        for (int j = 0; j < kBatch; ++j) {
             // a part without keys of the row (m = -inf) left nothing to read in O
-            if (k0 + j * kJoinGroups >= n || m[j] == -INFINITY) continue;
+            if (m[j] == -INFINITY) continue;
             const float w = exp2f(m[j] - M);
             t.lr += w * lr[j];
             t.le += w * le[j];
@@ -823,14 +823,14 @@ prefix_join_kernel(const __grid_constant__ PrefixParams p, int n_cta) {
 #pragma unroll
         for (int i = 0; i < kJoinCols; ++i) d[3 + i][r] = t.o[i];
     }
-    __syncthreads();
+    if (kGroups > 1) __syncthreads();
     if (grp > 0 || orow >= (long)p.R << p.hshift) return;
     float M = t.m;
 #pragma unroll
-    for (int j = 0; j < kJoinGroups - 1; ++j) M = fmaxf(M, sh[j][0][r]);
+    for (int j = 0; j < kGroups - 1; ++j) M = fmaxf(M, sh[j][0][r]);
     t.rescale(M);
 #pragma unroll
-    for (int j = 0; j < kJoinGroups - 1; ++j) {
+    for (int j = 0; j < kGroups - 1; ++j) {
         const float mk = sh[j][0][r];
         if (mk == -INFINITY) continue;
         const float w = exp2f(mk - M);
@@ -951,9 +951,17 @@ cudaError_t launch_attention_prefix_tc(const AttnArgs& a, void* workspace, uint3
     count_launch();
     e = cudaGetLastError();
     if (e != cudaSuccess || !cut) return e;
-    auto join = lse ? prefix_join_kernel<true> : prefix_join_kernel<false>;
-    // (launched in stream order: started early, its waiting CTAs cost the call 6 us)
-    join<<<(unsigned)(pl.U * (kD / kJoinCols)), kJoinGroups * kRows, 0, s>>>(p, pl.n_cta);
+    // (launched in stream order: started early, its waiting CTAs cost the call 6 us.
+    // With four threads a row throughout, one CTA fills an SM, and 101 units of 2 to 3
+    // parts took 20 us.)
+    const unsigned grid = (unsigned)(pl.U * (kD / kJoinCols));
+    if (pl.parts > 5) {
+        if (lse) prefix_join_kernel<true, 4, 5><<<grid, 4 * kRows, 0, s>>>(p, pl.n_cta);
+        else prefix_join_kernel<false, 4, 5><<<grid, 4 * kRows, 0, s>>>(p, pl.n_cta);
+    } else {
+        if (lse) prefix_join_kernel<true, 1, 3><<<grid, kRows, 0, s>>>(p, pl.n_cta);
+        else prefix_join_kernel<false, 1, 3><<<grid, kRows, 0, s>>>(p, pl.n_cta);
+    }
     count_launch();
     return cudaGetLastError();
 }
