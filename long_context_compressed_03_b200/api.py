@@ -141,9 +141,16 @@ def _dt_rot(t: torch.Tensor, rotated: bool) -> int:
     return d
 
 
-def _stream(stream) -> ctypes.c_void_p:
+# the current device and its current stream's handle, without a Stream object
+# (torch.cuda.current_stream() takes several us, as long as a small kernel)
+_device = getattr(torch._C, "_cuda_getDevice", None) or (lambda: torch.cuda.current_device())
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
+def _stream(stream):
     if stream is None:
-        stream = torch.cuda.current_stream()
+        return _raw_stream(_device())
     if isinstance(stream, torch.cuda.Stream):
         stream = stream.cuda_stream
     return ctypes.c_void_p(int(stream))
@@ -457,19 +464,23 @@ def hca_dense_attn_paged(q: torch.Tensor, kv_c: PagedCache, m: int, kv_raw: torc
 # ---------------------------------------------------------------- rotary positions
 def _same_device(t: torch.Tensor) -> None:
     """The library launches on the current device: refuse tensors of another one."""
-    if t.is_cuda and t.device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {t.device}, but the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
+    if t.is_cuda and t.get_device() != _device():
+        raise ValueError(f"tensors are on {t.device}, but the current device is cuda:{_device()}")
 
 
 def _shape(t: torch.Tensor | None, shape: tuple, name: str, dtype=None):
-    """Checks a tensor's shape (and dtype), then passes its pointer."""
-    if t is not None:
-        if tuple(t.shape) != shape:
-            raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
-        if dtype is not None and t.dtype != dtype:
-            raise ValueError(f"{name} must be {dtype}")
-    return _ptr(t)
+    """Checks a tensor's shape (and dtype), then passes its address."""
+    if t is None:
+        return None
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
+    if dtype is not None and t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}")
+    if not t.is_cuda:
+        raise ValueError("tensor arguments must be CUDA tensors")
+    if not t.is_contiguous():
+        raise ValueError("tensor arguments must be contiguous")
+    return t.data_ptr()
 
 
 def rope_freqs(d_rot: int, base: float = 10000.0, factor: float = 1.0, original_len: int = 0,
@@ -487,7 +498,29 @@ def rope_freqs(d_rot: int, base: float = 10000.0, factor: float = 1.0, original_
 _STRIDES = ctypes.c_longlong * 4
 
 
-def _rope_tensor(x: torch.Tensor | None, out: torch.Tensor | None, dims: tuple, name: str):
+def _rope_strides(x: torch.Tensor, out: torch.Tensor, name: str):
+    """{token, head} strides of x and of out, whose elements are n tokens apart."""
+    B, n, H, D = x.shape
+    st, spans = [], []
+    for t in (x, out):
+        s0, s1, s2, s3 = t.stride()
+        if t.is_contiguous():
+            s1, s2 = H * D, D
+        elif (D > 1 and s3 != 1) or (B > 1 and n > 0 and s0 != n * s1 and n != 1):
+            raise ValueError(f"{name}: channels must be contiguous and elements n tokens apart")
+        elif n == 1 and B > 1:
+            s1 = s0
+        st += [s1, s2]
+        e = t.element_size()
+        spans.append((t.data_ptr(), t.data_ptr() + ((B * n - 1) * s1 + (H - 1) * s2 + D) * e))
+    (a0, a1), (b0, b1) = spans
+    if a0 != b0 and a0 < b1 and b0 < a1 and x.numel():
+        # (views that interleave inside one buffer are refused too)
+        raise ValueError(f"the output of {name} overlaps it (give {name} itself to rotate in place)")
+    return _STRIDES(*st)
+
+
+def _rope_tensor(x: torch.Tensor | None, out: torch.Tensor | None, B: int, n: int, D: int, dt, name: str):
     """(x, out, heads, strides) arguments of csa_rope for one tensor [B, n, H, D]."""
     if x is None:
         if out is not None:
@@ -495,33 +528,20 @@ def _rope_tensor(x: torch.Tensor | None, out: torch.Tensor | None, dims: tuple, 
         return None, None, 0, None
     if out is None:
         raise ValueError(f"{name} needs an output")
-    B, n, D, dt = dims
-    if x.dim() != 4 or x.shape[0] != B or x.shape[1] != n or x.shape[3] != D or x.dtype != dt:
+    sh = x.shape
+    if len(sh) != 4 or sh[0] != B or sh[1] != n or sh[3] != D or x.dtype is not dt:
         raise ValueError(f"{name} must be [B, n, heads, D], of one shape and dtype with the other tensor")
-    if out.shape != x.shape or out.dtype != x.dtype:
+    if out.shape != sh or out.dtype is not dt:
         raise ValueError(f"the output of {name} must have its shape and dtype")
-    _same_device(x)
-    st = []
-    for t in (x, out):
-        if not t.is_cuda:
-            raise ValueError("tensor arguments must be CUDA tensors")
-        if t.is_contiguous():
-            st += [x.shape[2] * D, D]
-            continue
-        s0, s1, s2, s3 = t.stride()
-        if (D > 1 and s3 != 1) or (B > 1 and n > 0 and s0 != n * s1):
-            raise ValueError(f"{name}: channels must be contiguous and elements n tokens apart")
-        if n == 1 and B > 1:
-            s1 = s0
-        st += [s1, s2]
-    if out.data_ptr() != x.data_ptr() and x.numel():
-        # (ranges of the storage; views that interleave inside one buffer are refused too)
-        a0, b0, e = x.data_ptr(), out.data_ptr(), x.element_size()
-        a1 = a0 + ((B * n - 1) * st[0] + (x.shape[2] - 1) * st[1] + D) * e
-        b1 = b0 + ((B * n - 1) * st[2] + (x.shape[2] - 1) * st[3] + D) * e
-        if a0 < b1 and b0 < a1:
+    if not (x.is_cuda and out.is_cuda):
+        raise ValueError("tensor arguments must be CUDA tensors")
+    xp, op = x.data_ptr(), out.data_ptr()
+    if x.is_contiguous() and out.is_contiguous():
+        size = x.numel() * x.element_size()
+        if xp != op and xp < op + size and op < xp + size:
             raise ValueError(f"the output of {name} overlaps it (give {name} itself to rotate in place)")
-    return x.data_ptr(), out.data_ptr(), x.shape[2], _STRIDES(*st)
+        return xp, op, sh[2], None
+    return xp, op, sh[2], _rope_strides(x, out, name)
 
 
 def csa_rope(x: torch.Tensor, x_out: torch.Tensor, freqs: torch.Tensor,
@@ -535,17 +555,15 @@ def csa_rope(x: torch.Tensor, x_out: torch.Tensor, freqs: torch.Tensor,
     their channels are contiguous and their elements n tokens apart."""
     if x.dim() != 4:
         raise ValueError("x must be [B, n, heads, D]")
-    if freqs.dtype != torch.float64 or freqs.is_cuda or not freqs.is_contiguous() or freqs.dim() != 1:
+    if freqs.dtype is not torch.float64 or freqs.is_cuda or freqs.dim() != 1 or not freqs.is_contiguous():
         raise ValueError("freqs must be a contiguous float64 host tensor [d_rot / 2]")
     B, n, _, D = x.shape
-    dims = (B, n, D, x.dtype)
-    xa, xo, H, xs = _rope_tensor(x, x_out, dims, "x")
-    ya, yo, Hy, ys = _rope_tensor(y, y_out, dims, "y")
-    if pos is not None:
-        _i32(pos, "pos")
+    _same_device(x)
+    xa, xo, H, xs = _rope_tensor(x, x_out, B, n, D, x.dtype, "x")
+    ya, yo, Hy, ys = _rope_tensor(y, y_out, B, n, D, x.dtype, "y")
     _check(load().csa_rope(xa, xo, H, xs, ya, yo, Hy, ys, _dt(x), B, n, D, 2 * freqs.numel(),
-                           rot_offset, int(bool(interleaved)), freqs.data_ptr(), scale,
-                           _shape(pos, (B, n), "pos"), pos0, pos_step, int(bool(transpose)),
+                           rot_offset, interleaved, freqs.data_ptr(), scale,
+                           _shape(pos, (B, n), "pos", torch.int32), pos0, pos_step, transpose,
                            _stream(stream)))
 
 
@@ -563,10 +581,10 @@ def hca_dense_attn_prefix(q: torch.Tensor, kv_p: torch.Tensor, kv_c: torch.Tenso
     bytes; None takes one from torch's allocator, on the stream the call runs on."""
     B, n_q, H, D = q.shape
     _same_device(q)
-    if not (q.dtype == kv_p.dtype == kv_c.dtype == kv_raw.dtype == out.dtype):
+    if not (q.dtype is kv_p.dtype is kv_c.dtype is kv_raw.dtype is out.dtype):
         raise ValueError("q, kv_p, kv_c, kv_raw and out must share one dtype")
     N_p, N_cap, L = kv_p.shape[0], kv_c.shape[1], kv_raw.shape[1]
-    dt = _dt(q)
+    dt, i32 = _dt(q), torch.int32
     lib = load()
     if workspace is None:
         need = lib.hca_dense_attn_prefix_workspace(dt, B, n_q, H, D, N_p, N_cap, window)
@@ -575,12 +593,11 @@ def hca_dense_attn_prefix(q: torch.Tensor, kv_p: torch.Tensor, kv_c: torch.Tenso
     ws, wb = (workspace.data_ptr(), workspace.numel() * workspace.element_size()) \
         if workspace is not None else (None, 0)
     _check(lib.hca_dense_attn_prefix(
-        _ptr(q), dt, B, n_q, H, D, _shape(kv_p, (N_p, D), "kv_p"), N_p,
-        _shape(kv_c, (B, N_cap, D), "kv_c"), N_cap, _shape(n_entries, (B,), "n_entries", torch.int32),
-        m, _shape(kv_raw, (B, L, D), "kv_raw"), L, _shape(raw_pos0, (B,), "raw_pos0", torch.int32),
-        _shape(raw_len, (B,), "raw_len", torch.int32), window,
-        _shape(q_pos, (B, n_q), "q_pos", torch.int32), softmax_scale,
-        _shape(out, (B, n_q, H, D), "out"),
+        _shape(q, q.shape, "q"), dt, B, n_q, H, D, _shape(kv_p, (N_p, D), "kv_p"), N_p,
+        _shape(kv_c, (B, N_cap, D), "kv_c"), N_cap, _shape(n_entries, (B,), "n_entries", i32),
+        m, _shape(kv_raw, (B, L, D), "kv_raw"), L, _shape(raw_pos0, (B,), "raw_pos0", i32),
+        _shape(raw_len, (B,), "raw_len", i32), window, _shape(q_pos, (B, n_q), "q_pos", i32),
+        softmax_scale, _shape(out, (B, n_q, H, D), "out"),
         _shape(lse_out, (B, n_q, H), "lse_out", torch.float32), ws, wb, _stream(stream)))
 
 
@@ -609,7 +626,7 @@ def hca_entry_weights(q: torch.Tensor, kv_c: torch.Tensor, m: int, lse: torch.Te
     N_cap = kv_c.shape[1]
     topk = 0 if idx is None else idx.shape[-1]
     _check(load().hca_entry_weights(
-        _ptr(q), _dt(q), B, n_q, H, D, _shape(kv_c, (B, N_cap, D), "kv_c"), N_cap,
+        _shape(q, q.shape, "q"), _dt(q), B, n_q, H, D, _shape(kv_c, (B, N_cap, D), "kv_c"), N_cap,
         _shape(idx, (B, topk), "idx", torch.int32), topk,
         _shape(n_entries, (B,), "n_entries", torch.int32), m,
         _shape(q_pos, (B, n_q), "q_pos", torch.int32), softmax_scale,
@@ -695,8 +712,8 @@ def hca_attn(q, kv_c, m: int, kv_raw, window: int, with_lse: bool = False, **kw)
 
 def rope(x, freqs, pos=None, y=None, **kw):
     """Allocating form of csa_rope: (x rotated, y rotated or None)."""
-    out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    y_out = None if y is None else torch.empty(y.shape, dtype=y.dtype, device=y.device)
+    out = torch.empty_like(x, memory_format=torch.contiguous_format)
+    y_out = None if y is None else torch.empty_like(y, memory_format=torch.contiguous_format)
     csa_rope(x, out, freqs, y=y, y_out=y_out, pos=pos, **kw)
     return out, y_out
 

@@ -12,6 +12,8 @@
 // is then the exact phase of the rounded frequency, whole turns dropping out
 // by overflow, for any integer p.  Its top 32 bits feed sincospi: the angle
 // is within 2^-32 turns + 2^53 relative of the exact one.
+#include <algorithm>
+
 #include "common.cuh"
 #include "kernels.h"
 
@@ -19,12 +21,6 @@ namespace csa {
 namespace {
 
 constexpr int kThreads = 256;
-
-template <typename T>
-struct Vec {
-    static constexpr int N = 16 / sizeof(T);
-    T v[N];
-};
 
 // cos and sin of token `row`'s pairs for this CTA's tokens, cooperatively;
 // void tokens (position < 0) keep ok = 0 and are passed on unrotated.
@@ -44,6 +40,160 @@ __device__ __forceinline__ void fill_angles(const RopeArgs& a, long tok0, int n_
         if (j == 0) ok[t] = p >= 0;
     }
     __syncthreads();
+}
+
+// 16 bytes of a row as fp32, and back (rounded to nearest).
+__device__ __forceinline__ void unpack(const uint4& v, float* f, float) {
+    f[0] = __uint_as_float(v.x);
+    f[1] = __uint_as_float(v.y);
+    f[2] = __uint_as_float(v.z);
+    f[3] = __uint_as_float(v.w);
+}
+__device__ __forceinline__ void unpack(const uint4& v, float* f, __nv_bfloat16) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ uint4 pack(const float* f, float) {
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+}
+__device__ __forceinline__ uint4 pack(const float* f, __nv_bfloat16) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The rows of a CTA's tokens (tpb tokens and all their heads, or one token and
+// rpb of them), 16 bytes a step.  A thread keeps one item of a row -- a vector
+// (interleaved: its pairs are inside; not rotated: passed on), or in the half
+// layout the two vectors whose channels pair up -- and goes down the rows, kBatch
+// rows' loads in flight, the first of them under way while the angles are made.
+// Bound by HBM: every byte is read and written once.
+constexpr int kBatch = 4;
+
+template <typename T, bool HALF>
+__global__ void __launch_bounds__(kThreads) rope_vec_kernel(RopeArgs a, int tpb, int rpb, int chunks, int ipr) {
+    constexpr int V = 16 / sizeof(T);
+    extern __shared__ float2 cs[];
+    const int half = a.d_rot / 2;
+    int* ok = reinterpret_cast<int*>(cs + (size_t)tpb * half);
+    const long total = (long)a.B * a.n;
+    const long tok0 = (long)(blockIdx.x / chunks) * tpb;
+    const int r0 = (int)(blockIdx.x % chunks) * rpb;
+    const int n_tok = (int)min((long)tpb, total - tok0);
+    const int R = min(a.H[0] + a.H[1] - r0, rpb);
+    const int rot_items = (HALF ? half : a.d_rot) / V;
+    const int it = threadIdx.x % ipr, row_step = kThreads / ipr;
+    // the item's element offset in a row (HALF: of the first of its two vectors)
+    const bool rot = it < rot_items;
+    int e0 = a.off + it * V;
+    if (!rot) {
+        e0 = (it - rot_items) * V;
+        if (e0 >= a.off) e0 += a.d_rot;
+    }
+    const int pair0 = HALF ? it * V : it * (V / 2);
+    const int rows = (int)threadIdx.x < row_step * ipr ? n_tok * R : 0;    // (the last threads may have no item)
+    bool angles = false;
+    int rr0 = threadIdx.x / ipr;
+    do {
+        uint4 v[kBatch], w[kBatch];
+        T* dst[kBatch];
+        int tk[kBatch];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            const int rr = rr0 + b * row_step;
+            if (rr >= rows) continue;
+            const int t = tpb == 1 ? 0 : rr / R, h0 = r0 + rr - t * R;
+            const int which = h0 >= a.H[0];
+            const int h = which ? h0 - a.H[0] : h0;
+            const T* src = static_cast<const T*>(a.x[which]) + (tok0 + t) * a.xs[which][0] + h * a.xs[which][1] + e0;
+            dst[b] = static_cast<T*>(a.out[which]) + (tok0 + t) * a.os[which][0] + h * a.os[which][1] + e0;
+            tk[b] = t;
+            v[b] = *reinterpret_cast<const uint4*>(src);
+            if (HALF && rot) w[b] = *reinterpret_cast<const uint4*>(src + half);
+        }
+        if (!angles) {
+            fill_angles(a, tok0, n_tok, cs, ok);
+            angles = true;
+        }
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            if (rr0 + b * row_step >= rows) continue;
+            if (rot && ok[tk[b]]) {
+                const float2* c = cs + tk[b] * half + pair0;
+                float x[V], y[V];
+                unpack(v[b], x, T());
+                if (HALF) {
+                    unpack(w[b], y, T());
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        const float2 q = c[i];
+                        const float p0 = x[i] * q.x - y[i] * q.y, p1 = y[i] * q.x + x[i] * q.y;
+                        x[i] = p0;
+                        y[i] = p1;
+                    }
+                    w[b] = pack(y, T());
+                } else {
+#pragma unroll
+                    for (int i = 0; i < V / 2; ++i) {
+                        const float2 q = c[i];
+                        const float p0 = x[2 * i] * q.x - x[2 * i + 1] * q.y, p1 = x[2 * i + 1] * q.x + x[2 * i] * q.y;
+                        x[2 * i] = p0;
+                        x[2 * i + 1] = p1;
+                    }
+                }
+                v[b] = pack(x, T());
+            }
+            *reinterpret_cast<uint4*>(dst[b]) = v[b];
+            if (HALF && rot) *reinterpret_cast<uint4*>(dst[b] + half) = w[b];
+        }
+        rr0 += row_step * kBatch;
+    } while (rr0 < rows);
+}
+
+template <typename T>
+bool vec_supported(const RopeArgs& a) {
+    constexpr int V = 16 / sizeof(T);
+    if (a.D % V || a.off % V || (a.interleaved ? a.d_rot % V : a.d_rot / 2 % V)) return false;
+    if (a.D / V > kThreads) return false;
+    for (int w = 0; w < 2; ++w)
+        if (a.H[w] && (a.xs[w][0] % V || a.xs[w][1] % V || a.os[w][0] % V || a.os[w][1] % V)) return false;
+    return true;
+}
+
+template <typename T>
+cudaError_t launch_vec(const RopeArgs& a, cudaStream_t s) {
+    constexpr int V = 16 / sizeof(T);
+    const long total = (long)a.B * a.n;
+    const int R = a.H[0] + a.H[1];
+    // in place, the channels that are not rotated are already there
+    const bool in_place = (!a.H[0] || a.x[0] == a.out[0]) && (!a.H[1] || a.x[1] == a.out[1]);
+    const int ipr = (a.interleaved ? a.d_rot : a.d_rot / 2) / V + (in_place ? 0 : (a.D - a.d_rot) / V);
+    // Rows a CTA: one pass of kBatch a thread, fewer where the call has too few rows for
+    // the GPU (148 SMs, two CTAs each); whole tokens where a token's rows fit.
+    const int step = kThreads / ipr, pass = step * kBatch;
+    const int want = (int)std::min<long>(std::max<long>(total * R / (2 * 148), step), pass);
+    int tpb = 1, rpb = R, chunks = 1;
+    if (want >= R) {
+        tpb = std::max(1, std::min(want / R, 4096 / (a.d_rot / 2)));      // angles: 32 KB at most
+    } else {
+        chunks = (R + want - 1) / want;
+        rpb = (R + chunks - 1) / chunks;
+    }
+    const long blocks = (total + tpb - 1) / tpb * chunks;
+    if (blocks > (1L << 31) - 1) return cudaErrorInvalidConfiguration;
+    const size_t smem = (size_t)tpb * (a.d_rot / 2) * sizeof(float2) + tpb * sizeof(int);
+    auto kern = a.interleaved ? rope_vec_kernel<T, false> : rope_vec_kernel<T, true>;
+    kern<<<(unsigned)blocks, kThreads, smem, s>>>(a, tpb, rpb, chunks, ipr);
+    count_launch();
+    return cudaGetLastError();
 }
 
 // One pair or one passed-on element per thread and step: any size, stride and offset.
@@ -100,8 +250,9 @@ cudaError_t launch_scalar(const RopeArgs& a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_rope(const RopeArgs& a, cudaStream_t s) {
-    if (a.dt == DT_F32) return launch_scalar<float>(a, s);
-    return launch_scalar<__nv_bfloat16>(a, s);
+    // 16-byte items need sizes and strides that are whole vectors
+    if (a.dt == DT_F32) return vec_supported<float>(a) ? launch_vec<float>(a, s) : launch_scalar<float>(a, s);
+    return vec_supported<__nv_bfloat16>(a) ? launch_vec<__nv_bfloat16>(a, s) : launch_scalar<__nv_bfloat16>(a, s);
 }
 
 }  // namespace csa

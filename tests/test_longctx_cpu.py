@@ -89,7 +89,7 @@ def test_rope_binding_refusals(lib):
     with pytest.raises(ValueError, match="B, n, heads, D"):
         api.rope(x[0], f)
     with pytest.raises(ValueError, match="shape and dtype"):
-        api._rope_tensor(torch.zeros(1, 3, 1, 8), torch.zeros(1, 3, 1, 8), (1, 2, 8, x.dtype), "y")
+        api._rope_tensor(torch.zeros(1, 3, 1, 8), torch.zeros(1, 3, 1, 8), 1, 2, 8, x.dtype, "y")
     with pytest.raises(ValueError, match="shape and dtype"):
         api.csa_rope(x, torch.zeros(1, 2, 3, 7), f)
 
