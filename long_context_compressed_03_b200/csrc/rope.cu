@@ -70,16 +70,19 @@ __device__ __forceinline__ uint4 pack(const float* f, __nv_bfloat16) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// The rows of a CTA's tokens (tpb tokens and all their heads, or one token and
-// rpb of them), 16 bytes a step.  A thread keeps one item of a row -- a vector
+// 16 bytes a step: a CTA takes tpb tokens and all their rows (the heads of both
+// tensors, which share the angles), or rpb rows of one token.  A thread keeps one item of a row -- a vector
 // (interleaved: its pairs are inside; not rotated: passed on), or in the half
 // layout the two vectors whose channels pair up -- and goes down the rows, kBatch
 // rows' loads in flight, the first of them under way while the angles are made.
-// Bound by HBM: every byte is read and written once.
+// Bound by HBM: every byte is read and written once.  64 registers a thread (4
+// CTAs an SM) measured best: 122 us against 135 (3 CTAs) and 139 (5, spilling)
+// for 2 x 8192 tokens of 65 x 128 bf16.
 constexpr int kBatch = 4;
 
 template <typename T, bool HALF>
-__global__ void __launch_bounds__(kThreads) rope_vec_kernel(RopeArgs a, int tpb, int rpb, int chunks, int ipr) {
+__global__ void __launch_bounds__(kThreads, 4)
+rope_vec_kernel(const __grid_constant__ RopeArgs a, int tpb, int rpb, int chunks, int ipr) {
     constexpr int V = 16 / sizeof(T);
     extern __shared__ float2 cs[];
     const int half = a.d_rot / 2;
@@ -100,24 +103,24 @@ __global__ void __launch_bounds__(kThreads) rope_vec_kernel(RopeArgs a, int tpb,
     }
     const int pair0 = HALF ? it * V : it * (V / 2);
     const int rows = (int)threadIdx.x < row_step * ipr ? n_tok * R : 0;    // (the last threads may have no item)
+    // row rr of the CTA's: its address in the input / the output
+    const auto at = [&](int rr, int t, const void* const* ptr, const long(*st)[2]) {
+        const int h0 = r0 + rr - t * R;
+        const int w = h0 >= a.H[0];
+        return static_cast<const T*>(ptr[w]) + (tok0 + t) * st[w][0] + (w ? h0 - a.H[0] : h0) * st[w][1] + e0;
+    };
     bool angles = false;
     int rr0 = threadIdx.x / ipr;
     do {
         uint4 v[kBatch], w[kBatch];
-        T* dst[kBatch];
-        int tk[kBatch];
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
             const int rr = rr0 + b * row_step;
             if (rr >= rows) continue;
-            const int t = tpb == 1 ? 0 : rr / R, h0 = r0 + rr - t * R;
-            const int which = h0 >= a.H[0];
-            const int h = which ? h0 - a.H[0] : h0;
-            const T* src = static_cast<const T*>(a.x[which]) + (tok0 + t) * a.xs[which][0] + h * a.xs[which][1] + e0;
-            dst[b] = static_cast<T*>(a.out[which]) + (tok0 + t) * a.os[which][0] + h * a.os[which][1] + e0;
-            tk[b] = t;
-            v[b] = *reinterpret_cast<const uint4*>(src);
-            if (HALF && rot) w[b] = *reinterpret_cast<const uint4*>(src + half);
+            const int t = tpb == 1 ? 0 : rr / R;
+            const T* p = at(rr, t, a.x, a.xs);
+            v[b] = *reinterpret_cast<const uint4*>(p);
+            if (HALF && rot) w[b] = *reinterpret_cast<const uint4*>(p + half);
         }
         if (!angles) {
             fill_angles(a, tok0, n_tok, cs, ok);
@@ -125,9 +128,12 @@ __global__ void __launch_bounds__(kThreads) rope_vec_kernel(RopeArgs a, int tpb,
         }
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
-            if (rr0 + b * row_step >= rows) continue;
-            if (rot && ok[tk[b]]) {
-                const float2* c = cs + tk[b] * half + pair0;
+            const int rr = rr0 + b * row_step;
+            if (rr >= rows) continue;
+            const int t = tpb == 1 ? 0 : rr / R;
+            T* p = const_cast<T*>(at(rr, t, a.out, a.os));
+            if (rot && ok[t]) {
+                const float2* c = cs + t * half + pair0;
                 float x[V], y[V];
                 unpack(v[b], x, T());
                 if (HALF) {
@@ -151,8 +157,8 @@ __global__ void __launch_bounds__(kThreads) rope_vec_kernel(RopeArgs a, int tpb,
                 }
                 v[b] = pack(x, T());
             }
-            *reinterpret_cast<uint4*>(dst[b]) = v[b];
-            if (HALF && rot) *reinterpret_cast<uint4*>(dst[b] + half) = w[b];
+            *reinterpret_cast<uint4*>(p) = v[b];
+            if (HALF && rot) *reinterpret_cast<uint4*>(p + half) = w[b];
         }
         rr0 += row_step * kBatch;
     } while (rr0 < rows);
@@ -172,14 +178,17 @@ template <typename T>
 cudaError_t launch_vec(const RopeArgs& a, cudaStream_t s) {
     constexpr int V = 16 / sizeof(T);
     const long total = (long)a.B * a.n;
-    const int R = a.H[0] + a.H[1];
     // in place, the channels that are not rotated are already there
     const bool in_place = (!a.H[0] || a.x[0] == a.out[0]) && (!a.H[1] || a.x[1] == a.out[1]);
+    const int R = a.H[0] + a.H[1];
     const int ipr = (a.interleaved ? a.d_rot : a.d_rot / 2) / V + (in_place ? 0 : (a.D - a.d_rot) / V);
     // Rows a CTA: one pass of kBatch a thread, fewer where the call has too few rows for
-    // the GPU (148 SMs, two CTAs each); whole tokens where a token's rows fit.
+    // the GPU (148 SMs, two CTAs each); whole tokens where a token's rows fit.  With
+    // rows for 16 CTAs an SM, up to 8 passes: making one token's angles a CTA, by one
+    // warp, cost more than moving its rows.
     const int step = kThreads / ipr, pass = step * kBatch;
-    const int want = (int)std::min<long>(std::max<long>(total * R / (2 * 148), step), pass);
+    const int want = (int)std::max<long>(std::min<long>(std::max<long>(total * R / (2 * 148), step), pass),
+                                         std::min<long>(total * R / (16 * 148), 8L * pass));
     int tpb = 1, rpb = R, chunks = 1;
     if (want >= R) {
         tpb = std::max(1, std::min(want / R, 4096 / (a.d_rot / 2)));      // angles: 32 KB at most
