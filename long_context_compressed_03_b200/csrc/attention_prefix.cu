@@ -325,7 +325,12 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         const bool dead = *reinterpret_cast<volatile uint32_t*>(p.err) != 0u;
         ctl->abort = dead;
         ctl->q_ahead = !dead;
-        if (!dead) load_q(sQ, &tm_q, u0, &ctl->bar_q);
+    }
+    if (warp == 0) {
+        __syncwarp();
+        // (by an elected lane: TMA copies issued under a lane number took 200 cycles each)
+        if (__all_sync(0xffffffffu, *(volatile int*)&ctl->q_ahead != 0) && elect_one()) load_q(sQ, &tm_q, u0, &ctl->bar_q);
+        __syncwarp();
     }
     if (warp == kQkWarp) {
         tmem_alloc(&ctl->tmem_base, 512);
@@ -377,13 +382,14 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             if (g.lo < g.hi) do {
                 for (int i = g.lo; i < g.hi; ++i, ++L) {
                     const int slot = L % kStages, use = L / kStages;
-                    if (use > 0 && !wait_bar(&ctl->freeb[slot], (use - 1) & 1, abort, p.err, p.wait_ns)) { ok = false; break; }
-                    if (*abort) { ok = false; break; }
+                    if (use > 0) ok = wait(&ctl->freeb[slot], (use - 1) & 1);
+                    ok = __all_sync(0xffffffffu, ok && *abort == 0);
+                    if (!ok) break;
                     uint8_t* dst = sK + slot * kTileBytes;
                     uint64_t* bar = &ctl->full[slot];
                     bool copies = false, boxes = i < g.P;
                     if (i < g.P) {
-                        if (lt == 0) {
+                        if (warp == 0 && elect_one()) {
                             mbar_expect_tx(bar, kTileBytes);
                             for (int q = 0; q < 4; ++q)
                                 tma_load_2d(dst + (q & 1) * kHalf + (q >> 1) * kBox, &tm_p, (q & 1) * 64, i * kBN + (q >> 1) * 64, bar);
@@ -398,7 +404,7 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                             const bool w = j + 64 <= e1, pre = j >= e1 && j + 64 <= e2, own = j >= e2 && j + 64 <= e3;
                             if (w || pre || own) {
                                 boxes = true;
-                                if (lt == 0) {
+                                if (warp == 0 && elect_one()) {
                                     const CUtensorMap* m = w ? &tm_w : (pre ? &tm_p : &tm_c);
                                     const int y = w ? rw.b * p.a.L_raw + rw.win_lo + j
                                                     : (pre ? g.P * kBN + (j - e1) : rw.b * p.a.N_cap + (j - e2));
@@ -430,7 +436,6 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     else mbar_arrive(bar);
                 }
                 settle(true);
-                ok = __all_sync(0xffffffffu, ok);
                 if (ok) mode = next_mode(mode, &ok);
             } while (ok && mode != kFast);
         }

@@ -256,6 +256,11 @@ cudaError_t launch_entry_weights(const WeightsArgs& a, cudaStream_t s) {
         if (e != cudaSuccess) return e;
     }
     if ((a.idx ? a.topk : a.N_cap) == 0) return cudaSuccess;
+    if (entry_weights_tc_supported(a)) {
+        uint32_t* err = device_error_word();
+        if (!err) return cudaErrorUnknown;
+        return launch_entry_weights_tc(a, err, s);
+    }
     if (a.dt == DT_BF16 && a.D == 128) return launch_mma<128>(a, s);
     if (a.dt == DT_BF16 && a.D == 64) return launch_mma<64>(a, s);
     if (a.dt == DT_F32) return launch_simt<float>(a, s);

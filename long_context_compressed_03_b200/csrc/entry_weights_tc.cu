@@ -1,0 +1,553 @@
+// entry_weights_tc.cu -- the attention weight each compressed entry received, on
+// tcgen05 (see entry_weights.cu for the definition).
+//
+// The keys are the MMA's M: z^T = K.Q^T puts one key's scores against 128
+// (query row, head) columns into one TMEM lane, so a thread adds the weights of
+// one key over its columns in registers: no cross-lane sums, no atomics, and a
+// key that no row sees can hold anything, since it touches its own lane only.
+// Work item: 128 entries (or list slots) of one element, all columns in steps of
+// 128.  Persistent, one CTA per SM; item i is tile i / B of element i mod B, so the
+// tiles past the elements' ends come last and cost nothing.
+// Roles (24 warps): warp 0 loads Q and the entries' tiles (TMA); warps 1-2 stage
+// the columns' lse and reach; warps 3-6 gather listed entries row by row
+// (cp.async); warp 7 issues the MMAs; warps 8-23 take the four quarters of a
+// step's columns.  (One group of warps for all loads took 1800 cycles a step, most
+// of it waiting for its own instructions and lse, and 8 warps for the sums left
+// tensor-memory loads and exponentials one after the other: 47 us for 64 query
+// rows over 16384 entries.)
+// What bounds it: decode (one step an item) reads every key once, HBM; with many
+// query rows the exponentials, 1024 MUFU cycles a step against 512 of the tensor
+// pipe.  mma.sync ran at 150 TFLOP/s here, three times both bounds.
+#include <cudaTypedefs.h>
+
+#include <math.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "tc_common.cuh"
+
+namespace csa {
+namespace {
+
+using namespace tc;
+
+constexpr int kD = 128;
+constexpr int kKeys = 128;                  // entries of an item
+constexpr int kCols = 128;                  // columns of a step
+constexpr int kKBufs = 3, kStages = 3, kBufs = 4;
+constexpr int kHalf = 16384;                // 64 channels of 128 rows
+constexpr int kTileBytes = 2 * kHalf;
+constexpr int kTmaWarp = 0, kColWarp0 = 1, kColWarps = 2, kGatherWarp0 = 3, kGatherWarps = 4;
+constexpr int kMmaWarp = 7, kSumWarp0 = 8;
+constexpr int kGatherThreads = kGatherWarps * 32;
+constexpr int kQuarters = 4, kSumWarps = 4 * kQuarters;
+constexpr int kThreads = (kSumWarp0 + kSumWarps) * 32;
+constexpr int kNe = 1024;                   // elements whose entry count is kept in shared memory
+constexpr int kXs = 8;                      // items whose other quarters' sums may wait
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct __align__(16) Ctrl {
+    float nlse[kStages][kCols];             // -lse * log2(e) of the step's columns
+    int vis[kStages][kCols];                // entries the column's row sees (0: no column, empty row)
+    int low[kStages][kCols / 32];           // all of them, by 32 columns; -1: they differ
+    int ne[kNe];                            // the elements' entries
+    float xs[kXs][kQuarters - 1][kKeys];    // the other quarters' sums
+    uint64_t full[kStages], freeb[kStages];        // Q
+    uint64_t lfull[kStages], lfree[kStages];       // the columns' lse and reach
+    uint64_t kfull[kKBufs], kfree[kKBufs];
+    uint64_t s_full[kBufs], s_free[kBufs];
+    uint64_t x_full[kXs];
+    uint64_t fin;
+    uint32_t tmem_base;
+    int abort;
+};
+constexpr size_t kSmem = 1024 + (kKBufs + kStages) * kTileBytes + sizeof(Ctrl);
+
+struct TcWeights {
+    WeightsArgs a;
+    int chunks, items, steps, cols;
+    int hshift, mshift;          // log2 of H and m where they are powers of two, else -1
+    int qbox;                    // Q rows a TMA copy brings: 64 where no step has more columns, else 128
+    float sl2;
+    uint32_t* err;
+    uint64_t wait_ns;
+};
+
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* err,
+                                       uint64_t limit_ns) {
+    return mbar_wait(bar, parity, abort, err, limit_ns);
+}
+__device__ __forceinline__ bool elect_one() {
+    uint32_t on;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "elect.sync _|p, 0xffffffff;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(on));
+    return on != 0;
+}
+__device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
+    asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint64_t f2_pack(float lo, float hi) {
+    return (uint64_t)__float_as_uint(lo) | ((uint64_t)__float_as_uint(hi) << 32);
+}
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ float f2lo(uint64_t v) { return __uint_as_float((uint32_t)v); }
+__device__ __forceinline__ float f2hi(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
+
+// Sum of exp2(z * sl2 + nlse) over N columns of this thread's TMEM lane.
+template <int N>
+__device__ __forceinline__ float sum_columns(uint32_t taddr, const float* nlse, uint64_t sl2) {
+    float z[N];
+    if constexpr (N == 32) tmem_ld32(taddr, z);
+    else tmem_ld16(taddr, z);
+    uint64_t acc0 = 0, acc1 = 0;
+#pragma unroll
+    for (int e = 0; e < N; e += 4) {
+        const float4 l = *reinterpret_cast<const float4*>(nlse + e);
+        const uint64_t x0 = f2_fma(f2_pack(z[e], z[e + 1]), sl2, f2_pack(l.x, l.y));
+        const uint64_t x1 = f2_fma(f2_pack(z[e + 2], z[e + 3]), sl2, f2_pack(l.z, l.w));
+        acc0 = f2_add(acc0, f2_pack(ex2(f2lo(x0)), ex2(f2hi(x0))));
+        acc1 = f2_add(acc1, f2_pack(ex2(f2lo(x1)), ex2(f2hi(x1))));
+    }
+    acc0 = f2_add(acc0, acc1);
+    return f2lo(acc0) + f2hi(acc0);
+}
+
+// Item i of the grid: its element, tile and whether any key of it can be seen.
+struct Item {
+    int b, chunk, ne;
+    bool live;
+};
+__device__ __forceinline__ int entries_of(const WeightsArgs& a, int b) {
+    return clampi(a.n_entries ? __ldg(a.n_entries + b) : a.N_cap, 0, a.N_cap);
+}
+__device__ __forceinline__ Item item_of(const TcWeights& p, const int* ne, int i) {
+    Item t;
+    t.chunk = i / p.a.B;
+    t.b = i - t.chunk * p.a.B;
+    t.ne = t.b < kNe ? ne[t.b] : entries_of(p.a, t.b);
+    t.live = p.steps > 0 && (p.a.idx ? t.ne > 0 : t.chunk * kKeys < t.ne);
+    return t;
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+weights_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_q,
+                  const __grid_constant__ TcWeights p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* sK = base;                                  // [kKBufs][32 KB]
+    uint8_t* sQ = sK + kKBufs * kTileBytes;              // [kStages][32 KB]
+    Ctrl* ctl = reinterpret_cast<Ctrl*>(sQ + kStages * kTileBytes);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    volatile int* abort = &ctl->abort;
+    const WeightsArgs& a = p.a;
+    auto try_wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+        return mbar_try_wait(bar, parity) || wait_slow(bar, parity, abort, p.err, p.wait_ns);
+    };
+    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {       // by a whole warp
+        return __all_sync(0xffffffffu, try_wait(bar, parity));
+    };
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&ctl->full[i], 1);
+            mbar_init(&ctl->freeb[i], 1);
+            mbar_init(&ctl->lfull[i], kColWarps);
+            mbar_init(&ctl->lfree[i], kSumWarps);
+        }
+        for (int i = 0; i < kKBufs; ++i) {
+            mbar_init(&ctl->kfull[i], a.idx ? kGatherThreads : 1);
+            mbar_init(&ctl->kfree[i], 1);
+        }
+        for (int i = 0; i < kBufs; ++i) {
+            mbar_init(&ctl->s_full[i], 1);
+            mbar_init(&ctl->s_free[i], kSumWarps);
+        }
+        for (int i = 0; i < kXs; ++i) mbar_init(&ctl->x_full[i], kSumWarps - 4);
+        mbar_init(&ctl->fin, 1);
+        // a CTA started after another one timed out does no work
+        ctl->abort = (*reinterpret_cast<volatile uint32_t*>(p.err) != 0u) ? 1 : 0;
+        fence_barrier_init();
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(&ctl->tmem_base, kBufs * kCols);
+        tmem_relinquish();
+    }
+    for (int i = threadIdx.x; i < min(a.B, kNe); i += kThreads) ctl->ne[i] = entries_of(a, i);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = __shfl_sync(0xffffffffu, ctl->tmem_base, 0);
+
+    // the first live item at or after i, in this CTA's stride
+    const auto next_live = [&](int i, Item* t) -> int {
+        for (; i < p.items; i += gridDim.x) {
+            *t = item_of(p, ctl->ne, i);
+            if (t->live) break;
+        }
+        return i;
+    };
+    if (warp == kTmaWarp) {
+        // ------------------------------------------------------------ TMA: tiles and Q
+        int k = 0, L = 0;                    // live items, steps
+        bool ok = true;
+        Item t{};
+        for (int i = next_live(blockIdx.x, &t); i < p.items && ok; i = next_live(i + gridDim.x, &t), ++k) {
+            if (!a.idx) {
+                const int kb = k % kKBufs;
+                if (k >= kKBufs) ok = wait(&ctl->kfree[kb], (k / kKBufs - 1) & 1);
+                ok = __all_sync(0xffffffffu, ok && !*abort);
+                if (!ok) break;
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(&ctl->kfull[kb], kTileBytes);
+                    const int y = t.b * a.N_cap + t.chunk * kKeys;
+                    tma_load_2d(sK + kb * kTileBytes, &tm_k, 0, y, &ctl->kfull[kb]);
+                    tma_load_2d(sK + kb * kTileBytes + kHalf, &tm_k, 64, y, &ctl->kfull[kb]);
+                }
+                __syncwarp();
+            }
+            for (int st = 0; st < p.steps; ++st, ++L) {
+                const int sl = L % kStages;
+                if (L >= kStages) ok = wait(&ctl->freeb[sl], (L / kStages - 1) & 1);
+                ok = __all_sync(0xffffffffu, ok && !*abort);
+                if (!ok) break;
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(&ctl->full[sl], 2 * 128 * p.qbox);
+                    const int y = t.b * p.cols + st * kCols;
+                    tma_load_2d(sQ + sl * kTileBytes, &tm_q, 0, y, &ctl->full[sl]);
+                    tma_load_2d(sQ + sl * kTileBytes + kHalf, &tm_q, 64, y, &ctl->full[sl]);
+                }
+                __syncwarp();
+            }
+        }
+        // loads in flight land before the CTA's shared memory is given up
+        volatile int never = 0;
+        for (int q = 0; q < kStages; ++q)
+            if (L > q) mbar_wait(&ctl->full[q], ((L - 1 - q) / kStages) & 1, &never, p.err);
+        for (int q = 0; q < kKBufs; ++q)
+            if (!a.idx && k > q) mbar_wait(&ctl->kfull[q], ((k - 1 - q) / kKBufs) & 1, &never, p.err);
+        __syncwarp();
+    } else if (warp < kColWarp0 + kColWarps) {
+        // ------------------------------------------------------------ the columns
+        // Two columns a thread.  What a step needs is asked for one step ahead, into
+        // registers that the next step uses in place (two sets, taken in turn).
+        const int cw = warp - kColWarp0;
+        struct Col {
+            float lse[2];
+            int pos[2];
+            int ne;
+        };
+        const auto fetch = [&](const Item& t, int st) -> Col {
+            Col c;
+            c.ne = t.ne;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int at = st * kCols + 64 * cw + 32 * e + lane;
+                c.lse[e] = 0.0f;
+                c.pos[e] = -1;
+                if (at < p.cols) {
+                    const int qi = p.hshift >= 0 ? at >> p.hshift : at / a.H;
+                    c.pos[e] = a.q_pos ? __ldg(a.q_pos + (size_t)t.b * a.n_q + qi) : qi;
+                    c.lse[e] = __ldg(a.lse + (size_t)t.b * p.cols + at);
+                }
+            }
+            return c;
+        };
+        int L = 0;
+        bool ok = true;
+        const auto put = [&](const Col& col) -> bool {
+            const int sl = L % kStages;
+            if (L >= kStages) ok = wait(&ctl->lfree[sl], (L / kStages - 1) & 1);
+            if (!ok) return false;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float l = -col.lse[e] * kLog2e;
+                const unsigned n = (unsigned)col.pos[e] + 1u;
+                const int vis = (col.pos[e] < 0 || l == INFINITY) ? 0 : min((int)(p.mshift >= 0 ? n >> p.mshift : n / (unsigned)a.m), col.ne);
+                ctl->nlse[sl][64 * cw + 32 * e + lane] = l;
+                ctl->vis[sl][64 * cw + 32 * e + lane] = vis;
+                const int low = __reduce_min_sync(0xffffffffu, vis), high = __reduce_max_sync(0xffffffffu, vis);
+                if (lane == 0) ctl->low[sl][2 * cw + e] = low == high ? low : -1;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl->lfull[sl]);
+            ++L;
+            return true;
+        };
+        Item t{};
+        int i = next_live(blockIdx.x, &t), st = 0;
+        const auto advance = [&]() {
+            if (++st == p.steps) {
+                st = 0;
+                i = next_live(i + gridDim.x, &t);
+            }
+        };
+        Col c0, c1;
+        if (i < p.items) c0 = fetch(t, st);
+        while (i < p.items) {
+            advance();
+            const bool more = i < p.items;
+            if (more) c1 = fetch(t, st);
+            if (!put(c0) || !more) break;
+            advance();
+            if (i < p.items) c0 = fetch(t, st);
+            if (!put(c1)) break;
+        }
+    } else if (warp < kMmaWarp) {
+        // ------------------------------------------------------------ listed entries
+        // 16 lanes a row (an entry that is not in the cache: its first row, which the sums
+        // leave out).  An item's copies are handed over once the next item's are under way.
+        const int lt = threadIdx.x - kGatherWarp0 * 32, c16 = lt & 15;
+        int pend = -1;
+        const auto settle = [&](bool all) {
+            if (all) asm volatile("cp.async.wait_group 0;" ::: "memory");
+            else asm volatile("cp.async.wait_group 1;" ::: "memory");
+            if (pend >= 0) {
+                fence_proxy_async_smem();
+                mbar_arrive(&ctl->kfull[pend]);
+                pend = -1;
+            }
+        };
+        int k = 0;
+        bool ok = true;
+        Item t{};
+        for (int i = a.idx ? next_live(blockIdx.x, &t) : p.items; i < p.items && ok; ++k) {
+            const int kb = k % kKBufs;
+            constexpr int kPasses = kKeys * 16 / kGatherThreads;
+            int ent[kPasses];
+#pragma unroll
+            for (int it = 0; it < kPasses; ++it) {
+                const int j = t.chunk * kKeys + it * (kGatherThreads / 16) + (lt >> 4);
+                ent[it] = j < a.topk ? __ldg(a.idx + (size_t)t.b * a.topk + j) : 0;
+            }
+            const __nv_bfloat16* kv = static_cast<const __nv_bfloat16*>(a.kv_c) + (size_t)t.b * a.N_cap * kD + c16 * 8;
+            i = next_live(i + gridDim.x, &t);
+            if (k >= kKBufs) ok = wait(&ctl->kfree[kb], (k / kKBufs - 1) & 1);
+            ok = __all_sync(0xffffffffu, ok && !*abort);
+            if (!ok) break;
+            uint8_t* dk = sK + kb * kTileBytes + (c16 >> 3) * kHalf;
+#pragma unroll
+            for (int it = 0; it < kPasses; ++it) {
+                const int r = it * (kGatherThreads / 16) + (lt >> 4), s = (ent[it] >= 0 && ent[it] < a.N_cap) ? ent[it] : 0;
+                cp_async16(dk + r * 128 + (((c16 & 7) ^ (r & 7)) << 4), kv + (size_t)s * kD);
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            settle(false);
+            pend = kb;
+        }
+        settle(true);
+    } else if (warp == kMmaWarp) {
+        // ------------------------------------------------------------ z^T = K.Q^T
+        const uint64_t kd0 = sw128_desc(smem_u32(sK), 16, 1024), qd0 = sw128_desc(smem_u32(sQ), 16, 1024);
+        int k = 0, L = 0;
+        bool ok = true;
+        Item t{};
+        for (int i = next_live(blockIdx.x, &t); i < p.items && ok; i = next_live(i + gridDim.x, &t)) {
+            const int kb = k % kKBufs;
+            ok = wait(&ctl->kfull[kb], (k / kKBufs) & 1);
+            for (int st = 0; st < p.steps && ok; ++st, ++L) {
+                const int sl = L % kStages, buf = L % kBufs;
+                ok = (L < kBufs || wait(&ctl->s_free[buf], (L / kBufs - 1) & 1)) && wait(&ctl->full[sl], (L / kStages) & 1);
+                if (!ok) break;
+                tc_fence_after();
+                const int n = min(kCols, (p.cols - st * kCols + 15) & ~15);
+                const uint32_t id = idesc_bf16(kKeys, kCols, false, false) - ((uint32_t)((kCols - n) >> 3) << 17);
+                const uint64_t kd = kd0 + (uint64_t)(kb * (kTileBytes >> 4)), qd = qd0 + (uint64_t)(sl * (kTileBytes >> 4));
+                if (elect_one()) {
+#pragma unroll
+                    for (int kk = 0; kk < kD / 16; ++kk) {
+                        const uint32_t off16 = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
+                        mma_bf16_ss(tmem + buf * kCols, kd + off16, qd + off16, id, kk > 0);
+                    }
+                    mma_commit(&ctl->freeb[sl]);
+                    mma_commit(&ctl->s_full[buf]);
+                    if (st + 1 == p.steps) mma_commit(&ctl->kfree[kb]);
+                }
+                __syncwarp();
+            }
+            ++k;
+        }
+        if (elect_one()) mma_commit(&ctl->fin);
+        __syncwarp();
+        volatile int never = 0;
+        mbar_wait(&ctl->fin, 0, &never, p.err);
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------ weights and sums
+        const int h = (warp - kSumWarp0) >> 2;               // which quarter of a step's columns
+        const int r = (warp & 3) * 32 + lane;                // key of the item
+        const uint32_t my = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint64_t sl2 = f2_pack(p.sl2, p.sl2);
+        int k = 0, L = 0;
+        bool ok = true;
+        // an item's entry of this thread, and what it had (asked for one item ahead)
+        const auto entry = [&](const Item& t, float* had) -> int {
+            const int j = t.chunk * kKeys + r;
+            int s = a.idx ? (j < a.topk ? __ldg(a.idx + (size_t)t.b * a.topk + j) : -1) : j;
+            if (s < 0 || s >= a.N_cap) s = -1;
+            *had = 0.0f;
+            if (h == 0 && !a.idx && s >= 0 && a.in) *had = a.in[(size_t)t.b * a.N_cap + s];
+            return s;
+        };
+        Item tn{};
+        float had_n = 0.0f;
+        int s_n = -1;
+        if ((int)blockIdx.x < p.items) {
+            tn = item_of(p, ctl->ne, blockIdx.x);
+            s_n = entry(tn, &had_n);
+        }
+        for (int i = blockIdx.x; i < p.items && ok; i += gridDim.x) {
+            const Item t = tn;
+            const int s = s_n;
+            const float had = had_n;
+            float* dst = a.out + (size_t)t.b * a.N_cap + s;
+            if (i + (int)gridDim.x < p.items) {
+                tn = item_of(p, ctl->ne, i + gridDim.x);
+                s_n = entry(tn, &had_n);
+            }
+            if (!__any_sync(0xffffffffu, t.live)) {
+                if (h == 0 && !a.idx && s >= 0) *dst = had;
+                continue;
+            }
+            float sum = 0.0f;
+            for (int st = 0; st < p.steps; ++st, ++L) {
+                const int sl = L % kStages, buf = L % kBufs;
+                // this quarter's columns of the step: 32, or a quarter of what the last step has
+                const int n = min(kCols, (p.cols - st * kCols + 63) & ~63) / kQuarters, c0 = n * h;
+                // every wait is warp-collective: the TMEM accesses below are .sync.aligned
+                ok = wait(&ctl->lfull[sl], (L / kStages) & 1) && wait(&ctl->s_full[buf], (L / kBufs) & 1);
+                if (!ok) break;
+                tc_fence_after();
+                // columns of one query row (or rows that see the same): one test for all
+                const int same = ctl->low[sl][c0 >> 5];
+                float part = 0.0f;
+                if (n == 32 && same >= 0) {
+                    part = sum_columns<32>(my + buf * kCols + c0, &ctl->nlse[sl][c0], sl2);
+                } else if (same >= 0) {
+                    part = sum_columns<16>(my + buf * kCols + c0, &ctl->nlse[sl][c0], sl2);
+                } else {
+#pragma unroll 1
+                    for (int c = c0; c < c0 + n; c += 16) {
+                        float z[16];
+                        tmem_ld16(my + buf * kCols + c, z);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const float w = ex2(fmaf(z[e], p.sl2, ctl->nlse[sl][c + e]));
+                            if (s < ctl->vis[sl][c + e]) part += w;
+                        }
+                    }
+                }
+                if (same < 0 || s < same) sum += part;       // (what a key may not add may be NaN)
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&ctl->s_free[buf]);
+                    mbar_arrive(&ctl->lfree[sl]);
+                }
+            }
+            if (!ok) break;
+            // the quarters' sums meet.  (The others are at most kBufs steps, so kBufs
+            // items, ahead: their slot of xs has been read.)
+            if (h > 0) {
+                ctl->xs[k % kXs][h - 1][r] = sum;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl->x_full[k % kXs]);
+            } else {
+                ok = wait(&ctl->x_full[k % kXs], (k / kXs) & 1);
+                if (!ok) break;
+#pragma unroll
+                for (int q = 0; q < kQuarters - 1; ++q) sum += ctl->xs[k % kXs][q][r];
+                if (s >= 0) {
+                    // (an entry listed twice receives its weight twice: equal terms, any order)
+                    if (a.idx) atomicAdd(dst, sum);
+                    else *dst = had + sum;
+                }
+            }
+            ++k;
+        }
+    }
+    // (the MMA warp waited for its final commit: no MMA is in flight)
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kMmaWarp) tmem_dealloc(tmem, kBufs * kCols);
+}
+
+// ---------------------------------------------------------------------- host
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn_weights() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        cudaDriverEntryPointQueryResult q;
+        void* f = nullptr;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+        return static_cast<PFN_cuTensorMapEncodeTiled_v12000>(nullptr);
+    }();
+    return fn;
+}
+
+// 2D bf16 tensor [rows, 128] with a 128-byte-swizzled box of {64, n}.
+bool make_map_weights(CUtensorMap* m, const void* ptr, uint64_t rows, int n) {
+    auto fn = encode_fn_weights();
+    if (!fn) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)kD, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)kD * 2};
+    cuuint32_t box[2] = {64, (cuuint32_t)n};
+    cuuint32_t estr[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+// Served here: bf16 rows of 128 channels.
+bool entry_weights_tc_supported(const WeightsArgs& a) {
+    return a.dt == DT_BF16 && a.D == kD && (long)a.B * a.n_q * a.H < (1L << 31) - 64 && a.n_q > 0;
+}
+
+cudaError_t launch_entry_weights_tc(const WeightsArgs& a, uint32_t* err, cudaStream_t s) {
+    CUtensorMap tm_k, tm_q;
+    TcWeights p;
+    p.qbox = a.n_q * a.H <= 64 ? 64 : kCols;
+    if (!make_map_weights(&tm_k, a.kv_c, (uint64_t)a.B * a.N_cap, kKeys) ||
+        !make_map_weights(&tm_q, a.q, (uint64_t)a.B * a.n_q * a.H, p.qbox))
+        return cudaErrorInvalidValue;
+    p.a = a;
+    p.cols = a.n_q * a.H;
+    p.steps = (p.cols + kCols - 1) / kCols;
+    p.chunks = ((a.idx ? a.topk : a.N_cap) + kKeys - 1) / kKeys;
+    const long items = (long)p.chunks * a.B;
+    if (items > (1L << 31) - 1 - 148) return cudaErrorInvalidConfiguration;
+    p.items = (int)items;
+    const auto log2_of = [](int v) { return (v & (v - 1)) ? -1 : 31 - __builtin_clz((unsigned)v); };
+    p.hshift = log2_of(a.H);
+    p.mshift = log2_of(a.m);
+    p.sl2 = a.scale * kLog2e;
+    p.err = err;
+    p.wait_ns = wait_limit_ns();
+    cudaError_t e = cudaFuncSetAttribute(weights_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    if (e != cudaSuccess) return e;
+    weights_tc_kernel<<<(unsigned)std::min<long>(items, 148), kThreads, kSmem, s>>>(tm_k, tm_q, p);
+    count_launch();
+    return cudaGetLastError();
+}
+
+}  // namespace csa

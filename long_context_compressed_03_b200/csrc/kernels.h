@@ -219,6 +219,9 @@ cudaError_t launch_attention_prefix_tc(const AttnArgs& a, void* workspace, uint3
 unsigned long long attention_prefix_workspace(const AttnArgs& a);
 cudaError_t launch_attention_prefix(const AttnArgs& a, void* workspace, cudaStream_t s,
                                     const char** why);
+// tcgen05 entry weights: bf16 rows of 128 channels.
+bool entry_weights_tc_supported(const WeightsArgs& a);
+cudaError_t launch_entry_weights_tc(const WeightsArgs& a, uint32_t* err, cudaStream_t s);
 cudaError_t launch_rope(const RopeArgs& a, cudaStream_t s);
 cudaError_t launch_entry_weights(const WeightsArgs& a, cudaStream_t s);
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s);
