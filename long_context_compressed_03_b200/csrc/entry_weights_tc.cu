@@ -45,6 +45,7 @@ constexpr int kGatherThreads = kGatherWarps * 32;
 constexpr int kQuarters = 4, kSumWarps = 4 * kQuarters;
 constexpr int kThreads = (kSumWarp0 + kSumWarps) * 32;
 constexpr int kNe = 1024;                   // elements whose entry count is kept in shared memory
+constexpr int kSms = 148;
 constexpr int kXs = 8;                      // items whose other quarters' sums may wait
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -67,7 +68,8 @@ constexpr size_t kSmem = 1024 + (kKBufs + kStages) * kTileBytes + sizeof(Ctrl);
 
 struct TcWeights {
     WeightsArgs a;
-    int chunks, items, steps, cols;
+    int items, steps, cols;
+    int dchunk, db;              // a grid's width in (tiles, elements)
     int hshift, mshift;          // log2 of H and m where they are powers of two, else -1
     int qbox;                    // Q rows a TMA copy brings: 64 where no step has more columns, else 128
     float sl2;
@@ -88,6 +90,14 @@ __device__ __forceinline__ bool elect_one() {
 }
 __device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
     asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
+}
+// The rows of a map's box from row y on, both 64-column halves.
+__device__ __forceinline__ void tma_load_rows(void* dst, const CUtensorMap* m, int y, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];"
+        ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(m)), "r"(0), "r"(y), "r"(0), "r"(smem_u32(bar))
+        : "memory");
 }
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -129,21 +139,36 @@ __device__ __forceinline__ float sum_columns(uint32_t taddr, const float* nlse, 
     return f2lo(acc0) + f2hi(acc0);
 }
 
-// Item i of the grid: its element, tile and whether any key of it can be seen.
-struct Item {
-    int b, chunk, ne;
-    bool live;
-};
 __device__ __forceinline__ int entries_of(const WeightsArgs& a, int b) {
     return clampi(a.n_entries ? __ldg(a.n_entries + b) : a.N_cap, 0, a.N_cap);
 }
-__device__ __forceinline__ Item item_of(const TcWeights& p, const int* ne, int i) {
+// A CTA's items, one grid's width apart: tile i / B of element i mod B.
+struct Item {
+    int i, b, chunk, ne;
+    bool live;               // some key of it can be seen
+};
+__device__ __forceinline__ void look(const TcWeights& p, const int* ne, Item& t) {
+    t.ne = 0;
+    if (t.i < p.items) t.ne = t.b < kNe ? ne[t.b] : entries_of(p.a, t.b);
+    t.live = p.a.idx ? t.ne > 0 : t.chunk * kKeys < t.ne;
+}
+__device__ __forceinline__ Item first_item(const TcWeights& p, const int* ne) {
     Item t;
-    t.chunk = i / p.a.B;
-    t.b = i - t.chunk * p.a.B;
-    t.ne = t.b < kNe ? ne[t.b] : entries_of(p.a, t.b);
-    t.live = p.steps > 0 && (p.a.idx ? t.ne > 0 : t.chunk * kKeys < t.ne);
+    t.i = blockIdx.x;
+    t.chunk = t.i / p.a.B;
+    t.b = t.i - t.chunk * p.a.B;
+    look(p, ne, t);
     return t;
+}
+__device__ __forceinline__ void next_item(const TcWeights& p, const int* ne, Item& t) {
+    t.i += gridDim.x;
+    t.chunk += p.dchunk;
+    t.b += p.db;
+    if (t.b >= p.a.B) {
+        t.b -= p.a.B;
+        ++t.chunk;
+    }
+    look(p, ne, t);
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -195,20 +220,21 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, ctl->tmem_base, 0);
 
-    // the first live item at or after i, in this CTA's stride
-    const auto next_live = [&](int i, Item* t) -> int {
-        for (; i < p.items; i += gridDim.x) {
-            *t = item_of(p, ctl->ne, i);
-            if (t->live) break;
-        }
-        return i;
+    // the CTA's live items
+    const auto first_live = [&]() -> Item {
+        Item t = first_item(p, ctl->ne);
+        while (t.i < p.items && !t.live) next_item(p, ctl->ne, t);
+        return t;
+    };
+    const auto next_live = [&](Item& t) {
+        do next_item(p, ctl->ne, t);
+        while (t.i < p.items && !t.live);
     };
     if (warp == kTmaWarp) {
         // ------------------------------------------------------------ TMA: tiles and Q
         int k = 0, L = 0;                    // live items, steps
         bool ok = true;
-        Item t{};
-        for (int i = next_live(blockIdx.x, &t); i < p.items && ok; i = next_live(i + gridDim.x, &t), ++k) {
+        for (Item t = first_live(); t.i < p.items && ok; next_live(t), ++k) {
             if (!a.idx) {
                 const int kb = k % kKBufs;
                 if (k >= kKBufs) ok = wait(&ctl->kfree[kb], (k / kKBufs - 1) & 1);
@@ -217,8 +243,7 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 if (elect_one()) {
                     mbar_arrive_expect_tx(&ctl->kfull[kb], kTileBytes);
                     const int y = t.b * a.N_cap + t.chunk * kKeys;
-                    tma_load_2d(sK + kb * kTileBytes, &tm_k, 0, y, &ctl->kfull[kb]);
-                    tma_load_2d(sK + kb * kTileBytes + kHalf, &tm_k, 64, y, &ctl->kfull[kb]);
+                    tma_load_rows(sK + kb * kTileBytes, &tm_k, y, &ctl->kfull[kb]);
                 }
                 __syncwarp();
             }
@@ -229,9 +254,7 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 if (!ok) break;
                 if (elect_one()) {
                     mbar_arrive_expect_tx(&ctl->full[sl], 2 * 128 * p.qbox);
-                    const int y = t.b * p.cols + st * kCols;
-                    tma_load_2d(sQ + sl * kTileBytes, &tm_q, 0, y, &ctl->full[sl]);
-                    tma_load_2d(sQ + sl * kTileBytes + kHalf, &tm_q, 64, y, &ctl->full[sl]);
+                    tma_load_rows(sQ + sl * kTileBytes, &tm_q, t.b * p.cols + st * kCols, &ctl->full[sl]);
                 }
                 __syncwarp();
             }
@@ -290,23 +313,23 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             ++L;
             return true;
         };
-        Item t{};
-        int i = next_live(blockIdx.x, &t), st = 0;
+        Item t = first_live();
+        int st = 0;
         const auto advance = [&]() {
             if (++st == p.steps) {
                 st = 0;
-                i = next_live(i + gridDim.x, &t);
+                next_live(t);
             }
         };
         Col c0, c1;
-        if (i < p.items) c0 = fetch(t, st);
-        while (i < p.items) {
+        if (t.i < p.items) c0 = fetch(t, st);
+        while (t.i < p.items) {
             advance();
-            const bool more = i < p.items;
+            const bool more = t.i < p.items;
             if (more) c1 = fetch(t, st);
             if (!put(c0) || !more) break;
             advance();
-            if (i < p.items) c0 = fetch(t, st);
+            if (t.i < p.items) c0 = fetch(t, st);
             if (!put(c1)) break;
         }
     } else if (warp < kMmaWarp) {
@@ -326,8 +349,8 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         };
         int k = 0;
         bool ok = true;
-        Item t{};
-        for (int i = a.idx ? next_live(blockIdx.x, &t) : p.items; i < p.items && ok; ++k) {
+        Item t = first_live();
+        for (; a.idx && t.i < p.items && ok; ++k) {
             const int kb = k % kKBufs;
             constexpr int kPasses = kKeys * 16 / kGatherThreads;
             int ent[kPasses];
@@ -337,7 +360,7 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 ent[it] = j < a.topk ? __ldg(a.idx + (size_t)t.b * a.topk + j) : 0;
             }
             const __nv_bfloat16* kv = static_cast<const __nv_bfloat16*>(a.kv_c) + (size_t)t.b * a.N_cap * kD + c16 * 8;
-            i = next_live(i + gridDim.x, &t);
+            next_live(t);
             if (k >= kKBufs) ok = wait(&ctl->kfree[kb], (k / kKBufs - 1) & 1);
             ok = __all_sync(0xffffffffu, ok && !*abort);
             if (!ok) break;
@@ -357,8 +380,7 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         const uint64_t kd0 = sw128_desc(smem_u32(sK), 16, 1024), qd0 = sw128_desc(smem_u32(sQ), 16, 1024);
         int k = 0, L = 0;
         bool ok = true;
-        Item t{};
-        for (int i = next_live(blockIdx.x, &t); i < p.items && ok; i = next_live(i + gridDim.x, &t)) {
+        for (Item t = first_live(); t.i < p.items && ok; next_live(t)) {
             const int kb = k % kKBufs;
             ok = wait(&ctl->kfull[kb], (k / kKBufs) & 1);
             for (int st = 0; st < p.steps && ok; ++st, ++L) {
@@ -372,8 +394,9 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < kD / 16; ++kk) {
-                        const uint32_t off16 = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
-                        mma_bf16_ss(tmem + buf * kCols, kd + off16, qd + off16, id, kk > 0);
+                        const uint32_t off = (kk & 3) * 32;
+                        mma_bf16_ss(tmem + buf * kCols, kd + (((kk >> 2) * kHalf + off) >> 4),
+                                    qd + (((kk >> 2) * 128 * p.qbox + off) >> 4), id, kk > 0);
                     }
                     mma_commit(&ctl->freeb[sl]);
                     mma_commit(&ctl->s_full[buf]);
@@ -405,23 +428,17 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             if (h == 0 && !a.idx && s >= 0 && a.in) *had = a.in[(size_t)t.b * a.N_cap + s];
             return s;
         };
-        Item tn{};
+        Item tn = first_item(p, ctl->ne);
         float had_n = 0.0f;
-        int s_n = -1;
-        if ((int)blockIdx.x < p.items) {
-            tn = item_of(p, ctl->ne, blockIdx.x);
-            s_n = entry(tn, &had_n);
-        }
-        for (int i = blockIdx.x; i < p.items && ok; i += gridDim.x) {
+        int s_n = tn.i < p.items ? entry(tn, &had_n) : -1;
+        while (tn.i < p.items && ok) {
             const Item t = tn;
             const int s = s_n;
             const float had = had_n;
             float* dst = a.out + (size_t)t.b * a.N_cap + s;
-            if (i + (int)gridDim.x < p.items) {
-                tn = item_of(p, ctl->ne, i + gridDim.x);
-                s_n = entry(tn, &had_n);
-            }
-            if (!__any_sync(0xffffffffu, t.live)) {
+            next_item(p, ctl->ne, tn);
+            if (tn.i < p.items) s_n = entry(tn, &had_n);
+            if (!t.live) {
                 if (h == 0 && !a.idx && s >= 0) *dst = had;
                 continue;
             }
@@ -503,24 +520,29 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn_weights() {
     return fn;
 }
 
-// 2D bf16 tensor [rows, 128] with a 128-byte-swizzled box of {64, n}.
+// A bf16 tensor [rows, 128] as {64 channels, rows, 2 halves}, so that one copy brings n
+// rows as two 64-column halves, each 128-byte-swizzled (two copies took the loading
+// warp twice as long to issue).
 bool make_map_weights(CUtensorMap* m, const void* ptr, uint64_t rows, int n) {
     auto fn = encode_fn_weights();
     if (!fn) return false;
-    cuuint64_t dims[2] = {(cuuint64_t)kD, (cuuint64_t)rows};
-    cuuint64_t strides[1] = {(cuuint64_t)kD * 2};
-    cuuint32_t box[2] = {64, (cuuint32_t)n};
-    cuuint32_t estr[2] = {1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box, estr,
+    cuuint64_t dims[3] = {64, (cuuint64_t)rows, 2};
+    cuuint64_t strides[2] = {(cuuint64_t)kD * 2, 128};
+    cuuint32_t box[3] = {64, (cuuint32_t)n, 2};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, estr,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace
 
-// Served here: bf16 rows of 128 channels.
+// Served here: bf16 rows of 128 channels.  (Lists with a single step of columns go
+// to the mma.sync kernel, whose many small CTAs hide the gather better: 12.7 us
+// against 15.1 for 64 lists of 1999 entries and 64 columns.)
 bool entry_weights_tc_supported(const WeightsArgs& a) {
-    return a.dt == DT_BF16 && a.D == kD && (long)a.B * a.n_q * a.H < (1L << 31) - 64 && a.n_q > 0;
+    return a.dt == DT_BF16 && a.D == kD && (long)a.B * a.n_q * a.H < (1L << 31) - kCols && a.n_q > 0 &&
+           (!a.idx || (long)a.n_q * a.H > kCols);
 }
 
 cudaError_t launch_entry_weights_tc(const WeightsArgs& a, uint32_t* err, cudaStream_t s) {
@@ -533,10 +555,12 @@ cudaError_t launch_entry_weights_tc(const WeightsArgs& a, uint32_t* err, cudaStr
     p.a = a;
     p.cols = a.n_q * a.H;
     p.steps = (p.cols + kCols - 1) / kCols;
-    p.chunks = ((a.idx ? a.topk : a.N_cap) + kKeys - 1) / kKeys;
-    const long items = (long)p.chunks * a.B;
-    if (items > (1L << 31) - 1 - 148) return cudaErrorInvalidConfiguration;
+    const long items = (long)(((a.idx ? a.topk : a.N_cap) + kKeys - 1) / kKeys) * a.B;
+    if (items > (1L << 31) - 1 - kSms) return cudaErrorInvalidConfiguration;
     p.items = (int)items;
+    const int grid = (int)std::min<long>(items, kSms);
+    p.dchunk = grid / a.B;
+    p.db = grid % a.B;
     const auto log2_of = [](int v) { return (v & (v - 1)) ? -1 : 31 - __builtin_clz((unsigned)v); };
     p.hshift = log2_of(a.H);
     p.mshift = log2_of(a.m);
@@ -545,7 +569,7 @@ cudaError_t launch_entry_weights_tc(const WeightsArgs& a, uint32_t* err, cudaStr
     p.wait_ns = wait_limit_ns();
     cudaError_t e = cudaFuncSetAttribute(weights_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
     if (e != cudaSuccess) return e;
-    weights_tc_kernel<<<(unsigned)std::min<long>(items, 148), kThreads, kSmem, s>>>(tm_k, tm_q, p);
+    weights_tc_kernel<<<(unsigned)grid, kThreads, kSmem, s>>>(tm_k, tm_q, p);
     count_launch();
     return cudaGetLastError();
 }

@@ -113,10 +113,179 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(EvictArgs a) {
     if (tid == 0 && a.n_kept) a.n_kept[b] = kept;
 }
 
+// ------------------------------------------------------------------ registers
+// One CTA per element, its keys held in registers: the weights are read once.
+// Radix select in digits of 12, 12 and 8 bits: 12 leading bits cut every power of
+// two into 16, so the first histogram's atomics spread over its bins; later rounds
+// touch only the boundary bin's keys, and end early once the bin has as many keys
+// as are still wanted.  What bounds it is instruction issue on the element's one
+// SM: sums over warps are taken by a lane a warp, and only the warp that has the
+// boundary looks into its bins.  (A cluster of four CTAs an element, summing its
+// histograms over distributed shared memory, took 28 us for 64 elements of 32768:
+// reading 16 KB from three peers alone was 5 us.)
+constexpr int kBins = 4096, kLastBins = 256;
+
+template <int NT, int kPer>
+__global__ void __launch_bounds__(NT) evict_regs_kernel(EvictArgs a) {
+    constexpr int NW = NT / 32, Q = kBins / NT / 4;          // warps; quads of bins a thread
+    __shared__ __align__(16) int hist[2 * kBins + kLastBins];
+    __shared__ int wsum[NW];
+    __shared__ int found[3];                                 // bin, keys above it, keys in it
+    __shared__ int wgt[NW], weq[NW];
+    const int b = blockIdx.x;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    float* w = a.weight + (size_t)b * a.N_cap;
+    const int V = clampi(a.n_entries ? a.n_entries[b] : a.N_cap, 0, a.N_cap);
+    int* idx = a.idx_out + (size_t)b * a.budget;
+    const int s0 = warp * (32 * kPer) + lane;  // entries s0 + 32 e: a warp's are consecutive
+    const bool idle = s0 - lane >= V;                        // the warp has no entry
+
+    // keys plus one; 0: not a candidate
+    uint32_t key[kPer];
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) key[e] = 0;
+    if (!idle) {
+        float x[kPer];                                       // all loads in flight
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) x[e] = s0 + 32 * e < V ? w[s0 + 32 * e] : -1.0f;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) {
+            uint32_t k = 0;
+            if (evict_key(x[e], s0 + 32 * e, V, a.recent, &k)) key[e] = k + 1;
+        }
+    }
+    for (int i = tid; i < (2 * kBins + kLastBins) / 4; i += NT) reinterpret_cast<int4*>(hist)[i] = make_int4(0, 0, 0, 0);
+    __syncthreads();
+
+    // T: the least key kept (plus one), with the bits below `shift` zero
+    uint32_t T = 0;
+    int need = a.budget, total = 0;
+    bool all = false, ties = false;
+    int shift = 20;
+#pragma unroll 1
+    for (int round = 0;; ++round) {
+        int* h = hist + round * kBins;
+        const int bins = shift == 0 ? kLastBins : kBins;
+        const uint32_t mask = bins - 1;
+        const int top = shift == 20 ? 32 : (shift == 8 ? 20 : 8);     // bits at and above it are settled
+        if (!idle) {
+#pragma unroll
+            for (int e = 0; e < kPer; ++e)
+                if (key[e] && (top == 32 || ((key[e] ^ T) >> (top & 31)) == 0)) atomicAdd(&h[(key[e] >> shift) & mask], 1);
+        }
+        __syncthreads();
+        // thread t has the 4 Q bins from b0 on; the highest bins are the first thread's
+        const int b0 = 4 * Q * (NT - 1 - tid);
+        int4 cnt[Q];
+        int mine = 0;
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            cnt[q] = make_int4(0, 0, 0, 0);
+            if (b0 + 4 * q >= bins) continue;
+            cnt[q] = *reinterpret_cast<const int4*>(h + b0 + 4 * q);
+            mine += cnt[q].x + cnt[q].y + cnt[q].z + cnt[q].w;
+        }
+        const int of_warp = __reduce_add_sync(0xffffffffu, mine);
+        if (lane == 0) wsum[warp] = of_warp;
+        __syncthreads();
+        const int ws = lane < NW ? wsum[lane] : 0;
+        int above = __reduce_add_sync(0xffffffffu, lane < warp ? ws : 0);
+        if (round == 0) {
+            total = __reduce_add_sync(0xffffffffu, ws);
+            all = total <= a.budget;
+            if (all || a.budget == 0) break;
+        }
+        if (above < need && above + of_warp >= need) {       // this warp's bins have the boundary
+            int run = mine;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, run, o);
+                if (lane >= o) run += v;
+            }
+            above += run - mine;
+            if (above < need && above + mine >= need) {
+#pragma unroll
+                for (int q = Q - 1; q >= 0; --q) {
+                    const int v[4] = {cnt[q].w, cnt[q].z, cnt[q].y, cnt[q].x};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        if (above < need && above + v[j] >= need) {
+                            found[0] = b0 + 4 * q + 3 - j;
+                            found[1] = above;
+                            found[2] = v[j];
+                        }
+                        above += v[j];
+                    }
+                }
+            }
+        }
+        __syncthreads();
+        T |= (uint32_t)found[0] << shift;
+        need -= found[1];
+        if (found[2] == need) break;                         // all of the bin
+        if (shift == 0) {
+            ties = true;                                     // the first `need` of equal keys
+            break;
+        }
+        shift = shift == 20 ? 8 : 0;
+    }
+    // kept: every candidate; or the keys from T on; or those above T and `need` equals
+    const uint32_t from = all ? 1u : (a.budget == 0 ? 0xffffffffu : (ties ? T + 1 : T));
+    int gt = 0, eq = 0;
+    if (!idle) {
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) gt += key[e] >= from;
+        gt = __reduce_add_sync(0xffffffffu, gt);
+        if (ties) {
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) eq += key[e] == T;
+            eq = __reduce_add_sync(0xffffffffu, eq);
+        }
+    }
+    if (lane == 0) {
+        wgt[warp] = gt;
+        weq[warp] = eq;
+    }
+    __syncthreads();
+    int g0, e0;
+    {
+        const int x = lane < NW ? wgt[lane] : 0, y = lane < NW ? weq[lane] : 0;
+        g0 = __reduce_add_sync(0xffffffffu, lane < warp ? x : 0);
+        e0 = __reduce_add_sync(0xffffffffu, lane < warp ? y : 0);
+    }
+    if (!idle) {
+        const uint32_t below = (1u << lane) - 1u;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) {
+            const int s = s0 + 32 * e;
+            const bool isg = key[e] >= from;
+            const uint32_t mg = __ballot_sync(0xffffffffu, isg);
+            bool keep = isg;
+            int at = g0 + __popc(mg & below);
+            if (ties) {
+                const uint32_t me = __ballot_sync(0xffffffffu, key[e] == T);
+                const int eb = e0 + __popc(me & below);      // equals of T before this entry
+                keep = keep || (key[e] == T && eb < need);
+                at += min(eb, need);
+                e0 += __popc(me);
+            }
+            if (keep && at < a.budget) idx[at] = s;
+            else if (s < V) w[s] = -1.0f;
+            g0 += __popc(mg);
+        }
+    }
+    const int kept = min(total, a.budget);
+    for (int j = kept + tid; j < a.budget; j += NT) idx[j] = -1;
+    if (tid == 0 && a.n_kept) a.n_kept[b] = kept;
+}
+
 }  // namespace
 
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s) {
-    evict_kernel<<<(unsigned)a.B, kThreads, 0, s>>>(a);
+    // in registers where a CTA of 256 or 1024 threads holds the entries
+    if (a.N_cap <= 256 * 16) evict_regs_kernel<256, 16><<<(unsigned)a.B, 256, 0, s>>>(a);
+    else if (a.N_cap <= 1024 * 32) evict_regs_kernel<1024, 32><<<(unsigned)a.B, 1024, 0, s>>>(a);
+    else
+        evict_kernel<<<(unsigned)a.B, kThreads, 0, s>>>(a);
     count_launch();
     return cudaGetLastError();
 }
