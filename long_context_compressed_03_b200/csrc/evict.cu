@@ -142,6 +142,7 @@ __global__ void __launch_bounds__(NT) evict_regs_kernel(EvictArgs a) {
 
     // keys plus one; 0: not a candidate
     uint32_t key[kPer];
+    uint32_t gone = 0;                                       // bit e: the entry is marked already
 #pragma unroll
     for (int e = 0; e < kPer; ++e) key[e] = 0;
     if (!idle) {
@@ -152,6 +153,7 @@ __global__ void __launch_bounds__(NT) evict_regs_kernel(EvictArgs a) {
         for (int e = 0; e < kPer; ++e) {
             uint32_t k = 0;
             if (evict_key(x[e], s0 + 32 * e, V, a.recent, &k)) key[e] = k + 1;
+            gone |= (x[e] == -1.0f ? 1u : 0u) << e;
         }
     }
     for (int i = tid; i < (2 * kBins + kLastBins) / 4; i += NT) reinterpret_cast<int4*>(hist)[i] = make_int4(0, 0, 0, 0);
@@ -166,12 +168,21 @@ __global__ void __launch_bounds__(NT) evict_regs_kernel(EvictArgs a) {
     for (int round = 0;; ++round) {
         int* h = hist + round * kBins;
         const int bins = shift == 0 ? kLastBins : kBins;
-        const uint32_t mask = bins - 1;
-        const int top = shift == 20 ? 32 : (shift == 8 ? 20 : 8);     // bits at and above it are settled
         if (!idle) {
+            // (the digits' shifts as constants)
+            if (round == 0) {
 #pragma unroll
-            for (int e = 0; e < kPer; ++e)
-                if (key[e] && (top == 32 || ((key[e] ^ T) >> (top & 31)) == 0)) atomicAdd(&h[(key[e] >> shift) & mask], 1);
+                for (int e = 0; e < kPer; ++e)
+                    if (key[e]) atomicAdd(&h[key[e] >> 20], 1);
+            } else if (round == 1) {
+#pragma unroll
+                for (int e = 0; e < kPer; ++e)
+                    if ((key[e] ^ T) >> 20 == 0 && key[e]) atomicAdd(&h[key[e] >> 8 & 4095u], 1);
+            } else {
+#pragma unroll
+                for (int e = 0; e < kPer; ++e)
+                    if ((key[e] ^ T) >> 8 == 0 && key[e]) atomicAdd(&h[key[e] & 255u], 1);
+            }
         }
         __syncthreads();
         // thread t has the 4 Q bins from b0 on; the highest bins are the first thread's
@@ -269,7 +280,7 @@ __global__ void __launch_bounds__(NT) evict_regs_kernel(EvictArgs a) {
                 e0 += __popc(me);
             }
             if (keep && at < a.budget) idx[at] = s;
-            else if (s < V) w[s] = -1.0f;
+            else if (s < V && !(gone >> e & 1u)) w[s] = -1.0f;
             g0 += __popc(mg);
         }
     }
