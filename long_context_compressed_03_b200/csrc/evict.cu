@@ -241,47 +241,53 @@ __global__ void __launch_bounds__(NT) evict_regs_kernel(EvictArgs a) {
     }
     // kept: every candidate; or the keys from T on; or those above T and `need` equals
     const uint32_t from = all ? 1u : (a.budget == 0 ? 0xffffffffu : (ties ? T + 1 : T));
-    int gt = 0, eq = 0;
+    // lane e gets the bits of the warp's e-th 32 entries: what is kept, and the equals of T
+    uint32_t kw = 0, ew = 0;
     if (!idle) {
 #pragma unroll
-        for (int e = 0; e < kPer; ++e) gt += key[e] >= from;
-        gt = __reduce_add_sync(0xffffffffu, gt);
+        for (int e = 0; e < kPer; ++e) {
+            const uint32_t m = __ballot_sync(0xffffffffu, key[e] >= from);
+            if (lane == e) kw = m;
+        }
         if (ties) {
 #pragma unroll
-            for (int e = 0; e < kPer; ++e) eq += key[e] == T;
-            eq = __reduce_add_sync(0xffffffffu, eq);
+            for (int e = 0; e < kPer; ++e) {
+                const uint32_t m = __ballot_sync(0xffffffffu, key[e] == T);
+                if (lane == e) ew = m;
+            }
         }
     }
-    if (lane == 0) {
+    int gt = __popc(kw), eq = __popc(ew);                    // inclusive over the lanes
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, gt, o), y = __shfl_up_sync(0xffffffffu, eq, o);
+        if (lane >= o) {
+            gt += x;
+            eq += y;
+        }
+    }
+    if (lane == 31) {
         wgt[warp] = gt;
         weq[warp] = eq;
     }
     __syncthreads();
-    int g0, e0;
-    {
-        const int x = lane < NW ? wgt[lane] : 0, y = lane < NW ? weq[lane] : 0;
-        g0 = __reduce_add_sync(0xffffffffu, lane < warp ? x : 0);
-        e0 = __reduce_add_sync(0xffffffffu, lane < warp ? y : 0);
-    }
+    const int gw = lane < warp ? wgt[lane] : 0, qw = lane < warp ? weq[lane] : 0;
+    const int g0 = __reduce_add_sync(0xffffffffu, gw) + gt - __popc(kw);
+    const int e0 = __reduce_add_sync(0xffffffffu, qw) + eq - __popc(ew);
     if (!idle) {
-        const uint32_t below = (1u << lane) - 1u;
+        if (ties) {                                          // the lane's share of the `need` first equals
+            uint32_t left = ew;
+            for (int i = e0; i < need && left; ++i) {
+                kw |= left & (0u - left);
+                left &= left - 1;
+            }
+        }
+        int at = g0 + (ties ? min(e0, need) : 0);
+        for (uint32_t m = kw; m; m &= m - 1, ++at)
+            if (at < a.budget) idx[at] = (s0 - lane) + 32 * lane + __ffs(m) - 1;
 #pragma unroll
         for (int e = 0; e < kPer; ++e) {
-            const int s = s0 + 32 * e;
-            const bool isg = key[e] >= from;
-            const uint32_t mg = __ballot_sync(0xffffffffu, isg);
-            bool keep = isg;
-            int at = g0 + __popc(mg & below);
-            if (ties) {
-                const uint32_t me = __ballot_sync(0xffffffffu, key[e] == T);
-                const int eb = e0 + __popc(me & below);      // equals of T before this entry
-                keep = keep || (key[e] == T && eb < need);
-                at += min(eb, need);
-                e0 += __popc(me);
-            }
-            if (keep && at < a.budget) idx[at] = s;
-            else if (s < V && !(gone >> e & 1u)) w[s] = -1.0f;
-            g0 += __popc(mg);
+            const bool kept = ties ? (__shfl_sync(0xffffffffu, kw, e) >> lane & 1u) : key[e] >= from;
+            if (!kept && !(gone >> e & 1u) && s0 + 32 * e < V) w[s0 + 32 * e] = -1.0f;
         }
     }
     const int kept = min(total, a.budget);
