@@ -144,7 +144,49 @@ def test_prefix_attention(dt, B, nq, H, D, Np, cap, W):
     check_prefix(prefix_case(B * 100 + Np, dt, B, nq, H, D, Np, cap, W), dt)
 
 
-@pytest.mark.parametrize("dt,H,D", [(BF, 64, 128), (BF, 128, 128), (F32, 8, 64)])
+@pytest.mark.parametrize("dt,B,nq,H,D,Np,cap,W", [
+    # each head count and width; rows that share clusters of 8, 4 and 2 CTAs, and rows alone
+    (BF, 2, 1, 16, 128, 4000, 30, 100), (BF, 1, 3, 32, 64, 2500, 7, 60), (BF, 2, 2, 64, 64, 1500, 33, 70),
+    (BF, 1, 2, 128, 64, 900, 10, 128), (BF, 2, 1, 8, 128, 1111, 5, 17), (BF, 2, 2, 8, 64, 64, 0, 0),
+    (BF, 40, 1, 8, 64, 130, 9, 33), (BF, 75, 2, 16, 64, 200, 9, 33), (BF, 150, 1, 8, 128, 70, 3, 8),
+    (BF, 4, 1, 32, 128, 0, 70, 20), (BF, 1, 1, 16, 128, 17000, 0, 0), (BF, 1, 1, 32, 128, 1, 0, 0),
+    (F32, 37, 1, 8, 64, 90, 30, 20), (F32, 74, 1, 16, 64, 65, 3, 8), (F32, 75, 2, 8, 64, 40, 3, 8),
+    (F32, 1, 1, 128, 128, 333, 5, 9), (F32, 1, 2, 32, 128, 0, 300, 5), (F32, 1, 1, 8, 128, 255, 0, 1)])
+def test_prefix_attention_of_other_heads(dt, B, nq, H, D, Np, cap, W):
+    check_prefix(prefix_case(B * 100 + Np + H, dt, B, nq, H, D, Np, cap, W, void=(B // 2,) if B > 2 else ()), dt)
+
+
+@pytest.mark.parametrize("H", [64, 128])
+@pytest.mark.parametrize("where", ["first tile", "shared", "own", "window"])
+@pytest.mark.parametrize("gap", [30.0, 80.0, 500.0])
+def test_prefix_score_far_above_the_first_ones(H, where, gap):
+    # one key whose score is `gap` powers of two above all others, the first key's among them:
+    # weights of 2^gap against it fit an fp32 sum, pass 2^64, or overflow
+    a = prefix_case(51, BF, 3, 2, H, 128, 900, 60, 100, m=4)
+    u = (torch.randint(0, 2, (128,), generator=gen(52), device=DEV) * 2 - 1).to(BF)
+    sign = torch.ones(H, 1, device=DEV, dtype=BF)
+    sign[1::2] = -1                                        # (every other head sees it far below)
+    a["q"] = (u * sign).expand_as(a["q"]).contiguous()
+    c = gap * math.log(2.0) / math.sqrt(128.0)             # u . (c u) / sqrt(128) = gap ln 2
+    far = (u.float() * c).to(BF)
+    a["n_entries"] = i32([960, 960, 950])
+    a["q_pos"] = i32([[3898, 3899]] * 3)
+    a["raw_pos0"] = i32([3899 - a["kv_raw"].shape[1] + 1] * 3)
+    for k in ("kv_p", "kv_c", "kv_raw"):
+        a[k] = a[k] * 0.25
+    if where == "first tile":
+        a["kv_p"][77] = far
+    elif where == "shared":
+        a["kv_p"][500] = far
+    elif where == "own":
+        a["kv_c"][1, 45] = far
+    else:
+        a["kv_raw"][2, 70] = far
+    check_prefix(a, BF)
+
+
+@pytest.mark.parametrize("dt,H,D", [(BF, 64, 128), (BF, 128, 128), (BF, 16, 64), (BF, 32, 128), (BF, 8, 128),
+                                    (F32, 8, 64)])
 def test_prefix_partial_visibility_empty_rows_and_poison(dt, H, D):
     # rows that see no key, only part of the prefix, no window, a cache slot before position 0;
     # whatever a row may not see is NaN or infinite
