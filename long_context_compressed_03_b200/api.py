@@ -15,6 +15,7 @@ and call the ABI functions.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -587,11 +588,11 @@ def hca_dense_attn_prefix(q: torch.Tensor, kv_p: torch.Tensor, kv_c: torch.Tenso
     dt, i32 = _dt(q), torch.int32
     lib = load()
     if workspace is None:
-        need = lib.hca_dense_attn_prefix_workspace(dt, B, n_q, H, D, N_p, N_cap, window)
-        if need:
-            workspace = _scratch(need, q.device, stream)
-    ws, wb = (workspace.data_ptr(), workspace.numel() * workspace.element_size()) \
-        if workspace is not None else (None, 0)
+        wb = _prefix_workspace(dt, B, n_q, H, D, N_p, N_cap, window)
+        workspace = _scratch(wb, q.device, stream) if wb else None
+    else:
+        wb = workspace.numel() * workspace.element_size()
+    ws = None if workspace is None else workspace.data_ptr()
     _check(lib.hca_dense_attn_prefix(
         _shape(q, q.shape, "q"), dt, B, n_q, H, D, _shape(kv_p, (N_p, D), "kv_p"), N_p,
         _shape(kv_c, (B, N_cap, D), "kv_c"), N_cap, _shape(n_entries, (B,), "n_entries", i32),
@@ -599,6 +600,12 @@ def hca_dense_attn_prefix(q: torch.Tensor, kv_p: torch.Tensor, kv_c: torch.Tenso
         _shape(raw_len, (B,), "raw_len", i32), window, _shape(q_pos, (B, n_q), "q_pos", i32),
         softmax_scale, _shape(out, (B, n_q, H, D), "out"),
         _shape(lse_out, (B, n_q, H), "lse_out", torch.float32), ws, wb, _stream(stream)))
+
+
+@functools.lru_cache(maxsize=1024)
+def _prefix_workspace(*sizes) -> int:
+    """(a function of the sizes alone)"""
+    return load().hca_dense_attn_prefix_workspace(*sizes)
 
 
 def _scratch(nbytes: int, device, stream) -> torch.Tensor:
@@ -719,15 +726,18 @@ def rope(x, freqs, pos=None, y=None, **kw):
 
 
 def hca_attn_prefix(q, kv_p, kv_c, m: int, kv_raw, window: int, with_lse: bool = False, **kw):
-    out = torch.empty_like(q)
-    lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device) if with_lse else None
+    out, lse = torch.empty_like(q), None
+    if with_lse:
+        B, n_q, H, _ = q.shape
+        lse = torch.empty(B, n_q, H, dtype=torch.float32, device=q.device)
     hca_dense_attn_prefix(q, kv_p, kv_c, m, kv_raw, window, out, lse_out=lse, **kw)
     return (out, lse) if with_lse else out
 
 
 def entry_weights(q, kv_c, m: int, lse, weight=None, **kw) -> torch.Tensor:
     """Allocating form of hca_entry_weights: weight (or 0) + what each entry received."""
-    out = torch.empty(kv_c.shape[:2], dtype=torch.float32, device=kv_c.device)
+    B, N_cap, _ = kv_c.shape
+    out = torch.empty(B, N_cap, dtype=torch.float32, device=kv_c.device)
     hca_entry_weights(q, kv_c, m, lse, out, weight_in=weight, **kw)
     return out
 
