@@ -82,7 +82,7 @@ constexpr int kMaxUnits = 32;               // units a CTA meets, at most
 struct __align__(8) Ctrl {
     uint64_t bar_q, q_free;
     uint64_t full[kStages], freeb[kStages];
-    uint64_t s_full[kBufs], p_ready[kBufs], s_free[kBufs];
+    uint64_t s_full[kBufs], p_ready[kBufs][2], s_free[kBufs];   // p_ready: by 64-key half
     uint64_t o_full, o_free;
     uint64_t m_ready;        // the rows' offsets are there
     uint64_t done;           // every warp is through with the attempt
@@ -310,7 +310,8 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         }
         for (int i = 0; i < kBufs; ++i) {
             mbar_init(&ctl->s_full[i], 1);
-            mbar_init(&ctl->p_ready[i], kSoftWarps / 2);
+            mbar_init(&ctl->p_ready[i][0], kSoftWarps / 2);
+            mbar_init(&ctl->p_ready[i][1], kSoftWarps / 2);
             mbar_init(&ctl->s_free[i], 1);
         }
         mbar_init(&ctl->o_full, 1);
@@ -528,24 +529,30 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     const uint64_t vd = vd0 + (uint64_t)(slot * (kTileBytes >> 4));
                     const uint32_t a = tmem + buf * 128;
                     const uint32_t acc = i > 0;
-                    ok = wait(&ctl->p_ready[buf], (L / kBufs) & 1);
-                    if (!ok) break;
-                    tc_fence_after();
-                    if (elect_one()) {
-                        if (mode == kMax) {               // no weights yet: the tile and S are done with
-                            mbar_arrive(&ctl->freeb[slot]);
-                            mbar_arrive(&ctl->s_free[buf]);
-                        } else {
 #pragma unroll
-                            for (int kk = 0; kk < kBN / 16; ++kk)
-                                mma_bf16_ts(tmem + kOCol, a + (kk >> 2) * 64 + (kk & 3) * 8, vd + (uint64_t)(kk * (2048 >> 4)),
-                                            id_pv, kk > 0 ? 1u : acc);
-                            mma_commit(&ctl->freeb[slot]);
-                            mma_commit(&ctl->s_free[buf]);
-                            if (i + 1 == n) mma_commit(&ctl->o_full);
+                    for (int q = 0; q < 2; ++q) {
+                        ok = ok && wait(&ctl->p_ready[buf][q], (L / kBufs) & 1);
+                        if (!ok) break;
+                        tc_fence_after();
+                        if (elect_one()) {
+                            if (mode != kMax) {
+#pragma unroll
+                                for (int kk = 4 * q; kk < 4 * q + 4; ++kk)
+                                    mma_bf16_ts(tmem + kOCol, a + (kk >> 1) * 32 + (kk & 1) * 8,
+                                                vd + (uint64_t)(kk * (2048 >> 4)), id_pv, kk > 0 ? 1u : acc);
+                                if (q == 1) {
+                                    mma_commit(&ctl->freeb[slot]);
+                                    mma_commit(&ctl->s_free[buf]);
+                                    if (i + 1 == n) mma_commit(&ctl->o_full);
+                                }
+                            } else if (q == 1) {          // no weights yet: the tile and S are done with
+                                mbar_arrive(&ctl->freeb[slot]);
+                                mbar_arrive(&ctl->s_free[buf]);
+                            }
                         }
+                        __syncwarp();
                     }
-                    __syncwarp();
+                    if (!ok) break;
                 }
                 if (ok) mode = next_mode(mode, &ok);
             } while (ok && mode != kFast);
@@ -557,8 +564,10 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         __syncwarp();
     } else {
         // ------------------------------------------------------------ softmax and output
-        // Group gr takes every other tile; a row's 64-column half h of it is one
-        // thread's (id: which of the row's four threads).
+        // Group gr takes every other tile, thread h of a row 32 columns of each
+        // 64-key half (id: which of the row's four threads).  P V of a half
+        // starts when its P is there, which frees the buffer sooner: 1490 -> RESULT
+        // cycles a tile.
         const int gr = (warp - kSoftWarp0) >> 3, h = ((warp - kSoftWarp0) >> 2) & 1, id = 2 * gr + h;
         const int r = (warp & 3) * 32 + lane;                // row of the unit
         const uint32_t my = tmem + ((uint32_t)((warp & 3) * 32) << 16);
@@ -583,19 +592,28 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 #pragma unroll 1
                 for (; L_grp < L + n; L_grp += 2) {
                     const int buf = L_grp % kBufs, i = g.lo + (L_grp - L);
-                    const uint32_t s_addr = my + buf * 128 + 64 * h;
-                    // this half's columns that are keys of the row (the same in all lanes)
-                    int nv = 64;
+                    const uint32_t s_addr = my + buf * 128 + 32 * h;
+                    // the columns of each half that are keys of the row (the same in all lanes)
+                    int nvs = 32 | 32 << 8;
                     if (i >= g.P) {
-                        nv = own_len - (i - g.P) * H - (G == 1 ? 64 * h : 0);
-                        nv = (G == 2 && h != grp) ? 0 : max(min(nv, 64), 0);
+                        const int left = own_len - (i - g.P) * H - 32 * h;
+                        nvs = max(min(left, 32), 0);
+                        if (G == 2) nvs <<= 8 * grp;
+                        else nvs |= max(min(left - 64, 32), 0) << 8;
                     }
                     // every wait is warp-collective: the TMEM accesses below are .sync.aligned
                     ok = wait(&ctl->s_full[buf], (L_grp / kBufs) & 1);
                     if (!ok) break;
                     tc_fence_after();
                     if (mode == kMax) {
-                        if (nv > 0) top = fmaxf(top, row_max(s_addr, nv));
+#pragma unroll 1
+                        for (int q = 0; q < 2; ++q) {
+                            if (nvs & 255) top = fmaxf(top, row_max(s_addr + 64 * q, nvs & 255));
+                            nvs >>= 8;
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&ctl->p_ready[buf][q]);
+                        }
                     } else {
                         if (!have_m) {
                             // the row's first score in the first tile, from the group that has
@@ -615,22 +633,24 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                             m = ctl->m[r];
                             have_m = true;
                         }
-                        // P of this half's 64 keys, over the S it is made from
-                        if (nv > 0) {
-                            const float mm = (m == -INFINITY) ? 0.0f : m;
-                            const uint64_t sl2 = f2_pack(p.scale_log2, p.scale_log2), negm = f2_pack(-mm, -mm);
-                            uint64_t accr = 0, acce = 0;
-                            // (rolled: this much straight-line code would wait for its instructions)
+                        // P over the S it is made from
+                        const float mm = (m == -INFINITY) ? 0.0f : m;
+                        const uint64_t sl2 = f2_pack(p.scale_log2, p.scale_log2), negm = f2_pack(-mm, -mm);
+                        uint64_t accr = 0, acce = 0;
+                        // (rolled: this much straight-line code would wait for its instructions)
 #pragma unroll 1
-                            for (int q = 0; q < 2; ++q) {
+                        for (int q = 0; q < 2; ++q) {
+                            const int nv = nvs & 255;
+                            nvs >>= 8;
+                            if (nv > 0) {
+                                uint32_t pk[16];
                                 float sv[32];
-                                tmem_ld32(s_addr + 32 * q, sv);
-                                if (nv < 64) {
+                                tmem_ld32(s_addr + 64 * q, sv);
+                                if (nv < 32) {
 #pragma unroll
                                     for (int e = 0; e < 32; ++e)
-                                        if (32 * q + e >= nv) sv[e] = -INFINITY;
+                                        if (e >= nv) sv[e] = -INFINITY;
                                 }
-                                uint32_t pk[16];
 #pragma unroll
                                 for (int e = 0; e < 32; e += 2) {
                                     const uint64_t z = f2_fma(f2_pack(sv[e], sv[e + 1]), sl2, negm);
@@ -641,24 +661,23 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                                     accr = f2_add(accr, f2_pack(__uint_as_float(d << 16), __uint_as_float(d & 0xffff0000u)));
                                     if (LSE) acce = f2_add(acce, f2_pack(p0, p1));
                                 }
-                                tmem_st16(s_addr + 16 * q, pk);
-                            }
-                            const float sum = f2lo(accr) + f2hi(accr);
-                            large |= row.on && !(sum < kRange);
-                            l_r += sum;
-                            l_e += f2lo(acce) + f2hi(acce);
-                        } else {
-                            uint32_t zero[16];
+                                tmem_st16(s_addr + 64 * q, pk);
+                            } else {
+                                uint32_t zero[16];
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) zero[e] = 0u;
-                            tmem_st16(s_addr, zero);
-                            tmem_st16(s_addr + 16, zero);
+                                for (int e = 0; e < 16; ++e) zero[e] = 0u;
+                                tmem_st16(s_addr + 64 * q, zero);
+                            }
+                            tmem_st_wait();
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&ctl->p_ready[buf][q]);
                         }
-                        tmem_st_wait();
+                        const float sum = f2lo(accr) + f2hi(accr);
+                        large |= row.on && !(sum < kRange);
+                        l_r += sum;
+                        l_e += f2lo(acce) + f2hi(acce);
                     }
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&ctl->p_ready[buf]);
                 }
                 if (!ok) break;
                 L += n;
