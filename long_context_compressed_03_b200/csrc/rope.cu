@@ -71,20 +71,30 @@ __device__ __forceinline__ uint4 pack(const float* f, __nv_bfloat16) {
 }
 
 // 16 bytes a step: a CTA takes tpb tokens and all their rows (the heads of both
-// tensors, which share the angles), or rpb rows of one token.  A thread keeps one item of a row -- a vector
-// (interleaved: its pairs are inside; not rotated: passed on), or in the half
-// layout the two vectors whose channels pair up -- and goes down the rows, kBatch
-// rows' loads in flight, the first of them under way while the angles are made.
-// Bound by HBM: every byte is read and written once.  64 registers a thread (4
-// CTAs an SM) measured best: 122 us against 135 (3 CTAs) and 139 (5, spilling)
-// for 2 x 8192 tokens of 65 x 128 bf16.
-constexpr int kBatch = 4;
+// tensors, which share the angles), or rpb rows of one token.  A thread keeps one
+// item of a row -- a vector (interleaved: its pairs are inside; not rotated: passed
+// on), or in the half layout the two vectors whose channels pair up -- and goes
+// down the rows.  Its next kDepth - 1 rows are on their way to its own slots of
+// shared memory (cp.async, no barrier), the first of them while the angles are made.
+// Bound by HBM: every byte is read and written once.  2 x 8192 tokens of 65 x 128
+// bf16 take 90 us, 92% of a plain copy's rate; in batches of four rows through
+// registers, which drain before the next is asked for, 114 us.  Depths of 3, 6 and 8
+// took 94, 93 and 94 us.
+constexpr int kDepth = 4;
+template <bool HALF>
+__host__ __device__ constexpr size_t ring_bytes() { return (size_t)kDepth * kThreads * (HALF ? 32 : 16); }
+
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
+                 ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
+}
 
 template <typename T, bool HALF>
 __global__ void __launch_bounds__(kThreads, 4)
 rope_vec_kernel(const __grid_constant__ RopeArgs a, int tpb, int rpb, int chunks, int ipr) {
     constexpr int V = 16 / sizeof(T);
-    extern __shared__ float2 cs[];
+    extern __shared__ __align__(16) uint8_t smem[];
+    float2* cs = reinterpret_cast<float2*>(smem + ring_bytes<HALF>());
     const int half = a.d_rot / 2;
     int* ok = reinterpret_cast<int*>(cs + (size_t)tpb * half);
     const long total = (long)a.B * a.n;
@@ -103,65 +113,78 @@ rope_vec_kernel(const __grid_constant__ RopeArgs a, int tpb, int rpb, int chunks
     }
     const int pair0 = HALF ? it * V : it * (V / 2);
     const int rows = (int)threadIdx.x < row_step * ipr ? n_tok * R : 0;    // (the last threads may have no item)
-    // row rr of the CTA's: its address in the input / the output
-    const auto at = [&](int rr, int t, const void* const* ptr, const long(*st)[2]) {
-        const int h0 = r0 + rr - t * R;
-        const int w = h0 >= a.H[0];
-        return static_cast<const T*>(ptr[w]) + (tok0 + t) * st[w][0] + (w ? h0 - a.H[0] : h0) * st[w][1] + e0;
+    // the thread's rows, row_step apart: (token, row of it) of the next to load / to store
+    const int dt = row_step / R, dr = row_step - dt * R;
+    const int rr0 = threadIdx.x / ipr;
+    int lt = rr0 / R, lr = rr0 - lt * R, st = lt, sr = lr;
+    const auto step = [&](int& t, int& r) {
+        t += dt;
+        r += dr;
+        if (r >= R) {
+            r -= R;
+            ++t;
+        }
     };
-    bool angles = false;
-    int rr0 = threadIdx.x / ipr;
-    do {
-        uint4 v[kBatch], w[kBatch];
-#pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-            const int rr = rr0 + b * row_step;
-            if (rr >= rows) continue;
-            const int t = tpb == 1 ? 0 : rr / R;
-            const T* p = at(rr, t, a.x, a.xs);
-            v[b] = *reinterpret_cast<const uint4*>(p);
-            if (HALF && rot) w[b] = *reinterpret_cast<const uint4*>(p + half);
+    // where a row's item is in the input / the output
+    const auto at = [&](int t, int r, const void* const* ptr, const long(*sd)[2]) {
+        const int h0 = r0 + r;
+        const int w = h0 >= a.H[0];
+        return static_cast<const T*>(ptr[w]) + (tok0 + t) * sd[w][0] + (w ? h0 - a.H[0] : h0) * sd[w][1] + e0;
+    };
+    uint4* ring = reinterpret_cast<uint4*>(smem) + threadIdx.x;          // [kDepth][1 or 2][kThreads]
+    constexpr int kSlot = (HALF ? 2 : 1) * kThreads;
+    const int count = rows > rr0 ? (rows - rr0 + row_step - 1) / row_step : 0;
+    int loaded = 0;
+    const auto load = [&]() {
+        if (loaded < count) {
+            const T* p = at(lt, lr, a.x, a.xs);
+            uint4* d = ring + loaded % kDepth * kSlot;
+            cp_async16(d, p);
+            if (HALF && rot) cp_async16(d + kThreads, p + half);
+            step(lt, lr);
+            ++loaded;
         }
-        if (!angles) {
-            fill_angles(a, tok0, n_tok, cs, ok);
-            angles = true;
-        }
+        asm volatile("cp.async.commit_group;" ::: "memory");             // (one a step, if empty)
+    };
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-            const int rr = rr0 + b * row_step;
-            if (rr >= rows) continue;
-            const int t = tpb == 1 ? 0 : rr / R;
-            T* p = const_cast<T*>(at(rr, t, a.out, a.os));
-            if (rot && ok[t]) {
-                const float2* c = cs + t * half + pair0;
-                float x[V], y[V];
-                unpack(v[b], x, T());
-                if (HALF) {
-                    unpack(w[b], y, T());
+    for (int i = 0; i < kDepth - 1; ++i) load();
+    fill_angles(a, tok0, n_tok, cs, ok);
+    for (int k = 0; k < count; ++k) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 2) : "memory");
+        const uint4* d = ring + k % kDepth * kSlot;
+        uint4 v = d[0], w = make_uint4(0, 0, 0, 0);
+        if (HALF && rot) w = d[kThreads];
+        load();                                              // (into the slot read a step ago)
+        T* p = const_cast<T*>(at(st, sr, a.out, a.os));
+        if (rot && ok[st]) {
+            const float2* c = cs + st * half + pair0;
+            float x[V], y[V];
+            unpack(v, x, T());
+            if (HALF) {
+                unpack(w, y, T());
 #pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        const float2 q = c[i];
-                        const float p0 = x[i] * q.x - y[i] * q.y, p1 = y[i] * q.x + x[i] * q.y;
-                        x[i] = p0;
-                        y[i] = p1;
-                    }
-                    w[b] = pack(y, T());
-                } else {
-#pragma unroll
-                    for (int i = 0; i < V / 2; ++i) {
-                        const float2 q = c[i];
-                        const float p0 = x[2 * i] * q.x - x[2 * i + 1] * q.y, p1 = x[2 * i + 1] * q.x + x[2 * i] * q.y;
-                        x[2 * i] = p0;
-                        x[2 * i + 1] = p1;
-                    }
+                for (int i = 0; i < V; ++i) {
+                    const float2 q = c[i];
+                    const float p0 = x[i] * q.x - y[i] * q.y, p1 = y[i] * q.x + x[i] * q.y;
+                    x[i] = p0;
+                    y[i] = p1;
                 }
-                v[b] = pack(x, T());
+                w = pack(y, T());
+            } else {
+#pragma unroll
+                for (int i = 0; i < V / 2; ++i) {
+                    const float2 q = c[i];
+                    const float p0 = x[2 * i] * q.x - x[2 * i + 1] * q.y, p1 = x[2 * i + 1] * q.x + x[2 * i] * q.y;
+                    x[2 * i] = p0;
+                    x[2 * i + 1] = p1;
+                }
             }
-            *reinterpret_cast<uint4*>(p) = v[b];
-            if (HALF && rot) *reinterpret_cast<uint4*>(p + half) = w[b];
+            v = pack(x, T());
         }
-        rr0 += row_step * kBatch;
-    } while (rr0 < rows);
+        *reinterpret_cast<uint4*>(p) = v;
+        if (HALF && rot) *reinterpret_cast<uint4*>(p + half) = w;
+        step(st, sr);
+    }
 }
 
 template <typename T>
@@ -182,11 +205,11 @@ cudaError_t launch_vec(const RopeArgs& a, cudaStream_t s) {
     const bool in_place = (!a.H[0] || a.x[0] == a.out[0]) && (!a.H[1] || a.x[1] == a.out[1]);
     const int R = a.H[0] + a.H[1];
     const int ipr = (a.interleaved ? a.d_rot : a.d_rot / 2) / V + (in_place ? 0 : (a.D - a.d_rot) / V);
-    // Rows a CTA: one pass of kBatch a thread, fewer where the call has too few rows for
+    // Rows a CTA: kDepth a thread, fewer where the call has too few rows for
     // the GPU (148 SMs, two CTAs each); whole tokens where a token's rows fit.  With
-    // rows for 16 CTAs an SM, up to 8 passes: making one token's angles a CTA, by one
+    // rows for 16 CTAs an SM, up to 8 times that: making one token's angles a CTA, by one
     // warp, cost more than moving its rows.
-    const int step = kThreads / ipr, pass = step * kBatch;
+    const int step = kThreads / ipr, pass = step * kDepth;
     const int want = (int)std::max<long>(std::min<long>(std::max<long>(total * R / (2 * 148), step), pass),
                                          std::min<long>(total * R / (16 * 148), 8L * pass));
     int tpb = 1, rpb = R, chunks = 1;
@@ -198,8 +221,11 @@ cudaError_t launch_vec(const RopeArgs& a, cudaStream_t s) {
     }
     const long blocks = (total + tpb - 1) / tpb * chunks;
     if (blocks > (1L << 31) - 1) return cudaErrorInvalidConfiguration;
-    const size_t smem = (size_t)tpb * (a.d_rot / 2) * sizeof(float2) + tpb * sizeof(int);
+    const size_t smem = (a.interleaved ? ring_bytes<false>() : ring_bytes<true>()) +
+                        (size_t)tpb * (a.d_rot / 2) * sizeof(float2) + tpb * sizeof(int);
     auto kern = a.interleaved ? rope_vec_kernel<T, false> : rope_vec_kernel<T, true>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
     kern<<<(unsigned)blocks, kThreads, smem, s>>>(a, tpb, rpb, chunks, ipr);
     count_launch();
     return cudaGetLastError();
