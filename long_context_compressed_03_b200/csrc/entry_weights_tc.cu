@@ -50,15 +50,14 @@ constexpr int kXs = 8;                      // items whose other quarters' sums 
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct __align__(16) Ctrl {
-    float nlse[kStages][kCols];             // -lse * log2(e) of the step's columns
-    int vis[kStages][kCols];                // entries the column's row sees (0: no column, empty row)
-    int low[kStages][kCols / 32];           // all of them, by 32 columns; -1: they differ
+    float nlse[kBufs][kCols];               // -lse * log2(e) of the step's columns
+    int vis[kBufs][kCols];                  // entries the column's row sees (0: no column, empty row)
+    int low[kBufs][kCols / 32];             // all of them, by 32 columns; -1: they differ
     int ne[kNe];                            // the elements' entries
     float xs[kXs][kQuarters - 1][kKeys];    // the other quarters' sums
     uint64_t full[kStages], freeb[kStages];        // Q
-    uint64_t lfull[kStages], lfree[kStages];       // the columns' lse and reach
     uint64_t kfull[kKBufs], kfree[kKBufs];
-    uint64_t s_full[kBufs], s_free[kBufs];
+    uint64_t s_full[kBufs], s_free[kBufs];         // scores, and the columns' lse and reach
     uint64_t x_full[kXs];
     uint64_t fin;
     uint32_t tmem_base;
@@ -193,15 +192,13 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&ctl->full[i], 1);
             mbar_init(&ctl->freeb[i], 1);
-            mbar_init(&ctl->lfull[i], kColWarps);
-            mbar_init(&ctl->lfree[i], kSumWarps);
         }
         for (int i = 0; i < kKBufs; ++i) {
             mbar_init(&ctl->kfull[i], a.idx ? kGatherThreads : 1);
             mbar_init(&ctl->kfree[i], 1);
         }
         for (int i = 0; i < kBufs; ++i) {
-            mbar_init(&ctl->s_full[i], 1);
+            mbar_init(&ctl->s_full[i], 1 + kColWarps);
             mbar_init(&ctl->s_free[i], kSumWarps);
         }
         for (int i = 0; i < kXs; ++i) mbar_init(&ctl->x_full[i], kSumWarps - 4);
@@ -295,8 +292,8 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         int L = 0;
         bool ok = true;
         const auto put = [&](const Col& col) -> bool {
-            const int sl = L % kStages;
-            if (L >= kStages) ok = wait(&ctl->lfree[sl], (L / kStages - 1) & 1);
+            const int sl = L % kBufs;
+            if (L >= kBufs) ok = wait(&ctl->s_free[sl], (L / kBufs - 1) & 1);
             if (!ok) return false;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -309,7 +306,7 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 if (lane == 0) ctl->low[sl][2 * cw + e] = low == high ? low : -1;
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&ctl->lfull[sl]);
+            if (lane == 0) mbar_arrive(&ctl->s_full[sl]);
             ++L;
             return true;
         };
@@ -444,20 +441,20 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             }
             float sum = 0.0f;
             for (int st = 0; st < p.steps; ++st, ++L) {
-                const int sl = L % kStages, buf = L % kBufs;
+                const int buf = L % kBufs;
                 // this quarter's columns of the step: 32, or a quarter of what the last step has
                 const int n = min(kCols, (p.cols - st * kCols + 63) & ~63) / kQuarters, c0 = n * h;
                 // every wait is warp-collective: the TMEM accesses below are .sync.aligned
-                ok = wait(&ctl->lfull[sl], (L / kStages) & 1) && wait(&ctl->s_full[buf], (L / kBufs) & 1);
+                ok = wait(&ctl->s_full[buf], (L / kBufs) & 1);
                 if (!ok) break;
                 tc_fence_after();
                 // columns of one query row (or rows that see the same): one test for all
-                const int same = ctl->low[sl][c0 >> 5];
+                const int same = ctl->low[buf][c0 >> 5];
                 float part = 0.0f;
                 if (n == 32 && same >= 0) {
-                    part = sum_columns<32>(my + buf * kCols + c0, &ctl->nlse[sl][c0], sl2);
+                    part = sum_columns<32>(my + buf * kCols + c0, &ctl->nlse[buf][c0], sl2);
                 } else if (same >= 0) {
-                    part = sum_columns<16>(my + buf * kCols + c0, &ctl->nlse[sl][c0], sl2);
+                    part = sum_columns<16>(my + buf * kCols + c0, &ctl->nlse[buf][c0], sl2);
                 } else {
 #pragma unroll 1
                     for (int c = c0; c < c0 + n; c += 16) {
@@ -465,18 +462,15 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                         tmem_ld16(my + buf * kCols + c, z);
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
-                            const float w = ex2(fmaf(z[e], p.sl2, ctl->nlse[sl][c + e]));
-                            if (s < ctl->vis[sl][c + e]) part += w;
+                            const float w = ex2(fmaf(z[e], p.sl2, ctl->nlse[buf][c + e]));
+                            if (s < ctl->vis[buf][c + e]) part += w;
                         }
                     }
                 }
                 if (same < 0 || s < same) sum += part;       // (what a key may not add may be NaN)
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&ctl->s_free[buf]);
-                    mbar_arrive(&ctl->lfree[sl]);
-                }
+                if (lane == 0) mbar_arrive(&ctl->s_free[buf]);
             }
             if (!ok) break;
             // the quarters' sums meet.  (The others are at most kBufs steps, so kBufs
