@@ -448,7 +448,8 @@ csa_status_t hca_dense_attn_at(const void* q, int dt, int B, int n_q, int H, int
  *          the token stride); NULL: both contiguous [B, n, H, D].  Strides may
  *          be any non-negative numbers, but output heads and tokens must not overlap.
  *   x_out  may be x (with the same strides; then only the rotated channels are
- *          written); otherwise it must not overlap x or y.
+ *          written); otherwise outputs must not overlap x, y or one another (views of one
+ *          buffer that share its token stride and no channel are apart).
  *   dt     CSA_DT_F32 or CSA_DT_BF16, of every tensor.
  *   freqs  HOST double [d_rot / 2], radians a position (see csa_rope_freqs),
  *          |freqs| <= 10^6; read before the call returns.
@@ -526,7 +527,8 @@ csa_status_t hca_dense_attn_prefix(const void* q, int dt, int B, int n_q, int H,
  *   idx  [B, topk] int32: only the listed entries receive weight (the lists that
  *     csa_evict wrote and csa_sparse_attn attended to; negative values and
  *     values >= N_cap are skipped, an entry listed twice receives it twice);
- *     NULL: every visible entry.  The other entries keep what they had.
+ *     NULL: every visible entry.  The other entries keep what they had.  (After an
+ *     eviction give the list: without it an evicted entry's -1 receives weight too.)
  *   q [B, n_q, H, D], kv_c [B, N_cap, D]: dt CSA_DT_F32 or CSA_DT_BF16.
  *   lse [B, n_q, H] fp32;  q_pos [B, n_q] (NULL: q);  n_entries [B] (NULL: N_cap).
  *   weight_in [B, N_cap] fp32 or NULL (zeros); it may be weight_out, and must not

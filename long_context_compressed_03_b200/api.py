@@ -463,25 +463,35 @@ def hca_dense_attn_paged(q: torch.Tensor, kv_c: PagedCache, m: int, kv_raw: torc
 
 
 # ---------------------------------------------------------------- rotary positions
-def _same_device(t: torch.Tensor) -> None:
-    """The library launches on the current device: refuse tensors of another one."""
-    if t.is_cuda and t.get_device() != _device():
+def _same_device(t: torch.Tensor) -> int:
+    """t's device index (-1: the host).  The library launches on the current device:
+    tensors of another one are refused."""
+    dev = t.get_device()
+    if dev >= 0 and dev != _device():
         raise ValueError(f"tensors are on {t.device}, but the current device is cuda:{_device()}")
+    return dev
 
 
-def _shape(t: torch.Tensor | None, shape: tuple, name: str, dtype=None):
-    """Checks a tensor's shape (and dtype), then passes its address."""
+def _shape(t: torch.Tensor | None, shape: tuple, name: str, dev: int, dtype=None):
+    """Checks a tensor's shape (and dtype) and that it is on CUDA device ``dev``, then
+    passes its address."""
     if t is None:
         return None
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
     if dtype is not None and t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}")
-    if not t.is_cuda:
-        raise ValueError("tensor arguments must be CUDA tensors")
+    if dev < 0 or t.get_device() != dev:
+        _refuse_device(t, name, dev)
     if not t.is_contiguous():
         raise ValueError("tensor arguments must be contiguous")
     return t.data_ptr()
+
+
+def _refuse_device(t: torch.Tensor, name: str, dev: int):
+    if not t.is_cuda:
+        raise ValueError("tensor arguments must be CUDA tensors")
+    raise ValueError(f"{name} is on {t.device}, the first tensor on {'the host' if dev < 0 else f'cuda:{dev}'}")
 
 
 def rope_freqs(d_rot: int, base: float = 10000.0, factor: float = 1.0, original_len: int = 0,
@@ -521,7 +531,8 @@ def _rope_strides(x: torch.Tensor, out: torch.Tensor, name: str):
     return _STRIDES(*st)
 
 
-def _rope_tensor(x: torch.Tensor | None, out: torch.Tensor | None, B: int, n: int, D: int, dt, name: str):
+def _rope_tensor(x: torch.Tensor | None, out: torch.Tensor | None, B: int, n: int, D: int, dt, name: str,
+                 dev: int = -1):
     """(x, out, heads, strides) arguments of csa_rope for one tensor [B, n, H, D]."""
     if x is None:
         if out is not None:
@@ -534,8 +545,9 @@ def _rope_tensor(x: torch.Tensor | None, out: torch.Tensor | None, B: int, n: in
         raise ValueError(f"{name} must be [B, n, heads, D], of one shape and dtype with the other tensor")
     if out.shape != sh or out.dtype is not dt:
         raise ValueError(f"the output of {name} must have its shape and dtype")
-    if not (x.is_cuda and out.is_cuda):
-        raise ValueError("tensor arguments must be CUDA tensors")
+    for t in (x, out):
+        if dev < 0 or t.get_device() != dev:
+            _refuse_device(t, name, dev)
     xp, op = x.data_ptr(), out.data_ptr()
     if x.is_contiguous() and out.is_contiguous():
         size = x.numel() * x.element_size()
@@ -559,12 +571,12 @@ def csa_rope(x: torch.Tensor, x_out: torch.Tensor, freqs: torch.Tensor,
     if freqs.dtype is not torch.float64 or freqs.is_cuda or freqs.dim() != 1 or not freqs.is_contiguous():
         raise ValueError("freqs must be a contiguous float64 host tensor [d_rot / 2]")
     B, n, _, D = x.shape
-    _same_device(x)
-    xa, xo, H, xs = _rope_tensor(x, x_out, B, n, D, x.dtype, "x")
-    ya, yo, Hy, ys = _rope_tensor(y, y_out, B, n, D, x.dtype, "y")
+    dev = _same_device(x)
+    xa, xo, H, xs = _rope_tensor(x, x_out, B, n, D, x.dtype, "x", dev)
+    ya, yo, Hy, ys = _rope_tensor(y, y_out, B, n, D, x.dtype, "y", dev)
     _check(load().csa_rope(xa, xo, H, xs, ya, yo, Hy, ys, _dt(x), B, n, D, 2 * freqs.numel(),
                            rot_offset, interleaved, freqs.data_ptr(), scale,
-                           _shape(pos, (B, n), "pos", torch.int32), pos0, pos_step, transpose,
+                           _shape(pos, (B, n), "pos", dev, torch.int32), pos0, pos_step, transpose,
                            _stream(stream)))
 
 
@@ -581,25 +593,25 @@ def hca_dense_attn_prefix(q: torch.Tensor, kv_p: torch.Tensor, kv_c: torch.Tenso
     [B, N_cap, D].  ``workspace``: a CUDA tensor of hca_dense_attn_prefix_workspace(...)
     bytes; None takes one from torch's allocator, on the stream the call runs on."""
     B, n_q, H, D = q.shape
-    _same_device(q)
+    dev = _same_device(q)
     if not (q.dtype is kv_p.dtype is kv_c.dtype is kv_raw.dtype is out.dtype):
         raise ValueError("q, kv_p, kv_c, kv_raw and out must share one dtype")
     N_p, N_cap, L = kv_p.shape[0], kv_c.shape[1], kv_raw.shape[1]
     dt, i32 = _dt(q), torch.int32
     lib = load()
-    if workspace is None:
+    if workspace is None and dev >= 0:
         wb = _prefix_workspace(dt, B, n_q, H, D, N_p, N_cap, window)
         workspace = _scratch(wb, q.device, stream) if wb else None
     else:
-        wb = workspace.numel() * workspace.element_size()
-    ws = None if workspace is None else workspace.data_ptr()
+        wb = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    ws = None if workspace is None else _shape(workspace, workspace.shape, "workspace", dev)
     _check(lib.hca_dense_attn_prefix(
-        _shape(q, q.shape, "q"), dt, B, n_q, H, D, _shape(kv_p, (N_p, D), "kv_p"), N_p,
-        _shape(kv_c, (B, N_cap, D), "kv_c"), N_cap, _shape(n_entries, (B,), "n_entries", i32),
-        m, _shape(kv_raw, (B, L, D), "kv_raw"), L, _shape(raw_pos0, (B,), "raw_pos0", i32),
-        _shape(raw_len, (B,), "raw_len", i32), window, _shape(q_pos, (B, n_q), "q_pos", i32),
-        softmax_scale, _shape(out, (B, n_q, H, D), "out"),
-        _shape(lse_out, (B, n_q, H), "lse_out", torch.float32), ws, wb, _stream(stream)))
+        _shape(q, q.shape, "q", dev), dt, B, n_q, H, D, _shape(kv_p, (N_p, D), "kv_p", dev), N_p,
+        _shape(kv_c, (B, N_cap, D), "kv_c", dev), N_cap, _shape(n_entries, (B,), "n_entries", dev, i32),
+        m, _shape(kv_raw, (B, L, D), "kv_raw", dev), L, _shape(raw_pos0, (B,), "raw_pos0", dev, i32),
+        _shape(raw_len, (B,), "raw_len", dev, i32), window, _shape(q_pos, (B, n_q), "q_pos", dev, i32),
+        softmax_scale, _shape(out, (B, n_q, H, D), "out", dev),
+        _shape(lse_out, (B, n_q, H), "lse_out", dev, torch.float32), ws, wb, _stream(stream)))
 
 
 @functools.lru_cache(maxsize=1024)
@@ -627,19 +639,19 @@ def hca_entry_weights(q: torch.Tensor, kv_c: torch.Tensor, m: int, lse: torch.Te
     idx [B, topk]) entry of kv_c [B, N_cap, D] received from q [B, n_q, H, D], given the
     attention's lse [B, n_q, H]."""
     B, n_q, H, D = q.shape
-    _same_device(q)
+    dev = _same_device(q)
     if q.dtype != kv_c.dtype:
         raise ValueError("q and kv_c must share one dtype")
     N_cap = kv_c.shape[1]
     topk = 0 if idx is None else idx.shape[-1]
     _check(load().hca_entry_weights(
-        _shape(q, q.shape, "q"), _dt(q), B, n_q, H, D, _shape(kv_c, (B, N_cap, D), "kv_c"), N_cap,
-        _shape(idx, (B, topk), "idx", torch.int32), topk,
-        _shape(n_entries, (B,), "n_entries", torch.int32), m,
-        _shape(q_pos, (B, n_q), "q_pos", torch.int32), softmax_scale,
-        _shape(lse, (B, n_q, H), "lse", torch.float32),
-        _shape(weight_in, (B, N_cap), "weight_in", torch.float32),
-        _shape(weight_out, (B, N_cap), "weight_out", torch.float32), _stream(stream)))
+        _shape(q, q.shape, "q", dev), _dt(q), B, n_q, H, D, _shape(kv_c, (B, N_cap, D), "kv_c", dev), N_cap,
+        _shape(idx, (B, topk), "idx", dev, torch.int32), topk,
+        _shape(n_entries, (B,), "n_entries", dev, torch.int32), m,
+        _shape(q_pos, (B, n_q), "q_pos", dev, torch.int32), softmax_scale,
+        _shape(lse, (B, n_q, H), "lse", dev, torch.float32),
+        _shape(weight_in, (B, N_cap), "weight_in", dev, torch.float32),
+        _shape(weight_out, (B, N_cap), "weight_out", dev, torch.float32), _stream(stream)))
 
 
 def csa_evict(weight: torch.Tensor, budget: int, idx_out: torch.Tensor,
@@ -650,11 +662,11 @@ def csa_evict(weight: torch.Tensor, budget: int, idx_out: torch.Tensor,
     if weight.dim() != 2:
         raise ValueError("weight must be [B, N_cap]")
     B, N_cap = weight.shape
-    _same_device(weight)
-    _check(load().csa_evict(_shape(weight, (B, N_cap), "weight", torch.float32), B, N_cap,
-                            _shape(n_entries, (B,), "n_entries", torch.int32), budget, recent,
-                            _shape(idx_out, (B, budget), "idx_out", torch.int32),
-                            _shape(n_kept, (B,), "n_kept", torch.int32), _stream(stream)))
+    dev = _same_device(weight)
+    _check(load().csa_evict(_shape(weight, (B, N_cap), "weight", dev, torch.float32), B, N_cap,
+                            _shape(n_entries, (B,), "n_entries", dev, torch.int32), budget, recent,
+                            _shape(idx_out, (B, budget), "idx_out", dev, torch.int32),
+                            _shape(n_kept, (B,), "n_kept", dev, torch.int32), _stream(stream)))
 
 
 # ---------------------------------------------------------------- allocating wrappers

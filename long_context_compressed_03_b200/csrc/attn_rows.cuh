@@ -22,7 +22,7 @@ __device__ __forceinline__ RowKeys row_keys(const AttnArgs& a, int b, int t) {
     if (a.dense) {
         const int cap = a.N_p + a.N_cap;
         const int ne = clampi(a.n_entries ? a.n_entries[b] : cap, 0, cap);
-        k.n_comp = t < 0 ? 0 : min((t + 1) / a.m, ne);
+        k.n_comp = t < 0 ? 0 : (int)min((t + 1u) / (unsigned)a.m, (unsigned)ne);   // (t + 1 may be 2^31)
     } else {
         k.n_comp = a.topk;
     }

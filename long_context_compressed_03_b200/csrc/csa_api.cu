@@ -620,6 +620,17 @@ csa_status_t csa_rope_freqs(int d_rot, double base, double factor, int original_
     return ok();
 }
 
+// Two tensors of `total` tokens (token stride s, `ext` elements a token from p on) share
+// no element: their spans are apart, or (views of one buffer) they have one token
+// stride and different channels of it.
+static bool apart(const void* p, long sp, long ep, const void* q, long sq, long eq, long total, int size) {
+    const char *p0 = static_cast<const char*>(p), *q0 = static_cast<const char*>(q);
+    if (p0 + ((total - 1) * sp + ep) * size <= q0 || q0 + ((total - 1) * sq + eq) * size <= p0) return true;
+    if (sp != sq || sp == 0 || (q0 - p0) % size) return false;
+    const long d = (((q0 - p0) / size) % sp + sp) % sp;      // q's first channel in p's token
+    return d >= ep && d + eq <= sp;
+}
+
 csa_status_t csa_rope(const void* x, void* x_out, int H, const long long* x_strides,
                       const void* y, void* y_out, int H_y, const long long* y_strides, int dt,
                       int B, int n, int D, int d_rot, int rot_offset, int interleaved,
@@ -670,6 +681,22 @@ csa_status_t csa_rope(const void* x, void* x_out, int H, const long long* x_stri
     }
     REQUIRE_ALIGNED4(pos, "pos");
     if ((long)B * n * (H + H_y) == 0) return ok();
+    long ext[2][2];                                          // elements a token spans: input, output
+    for (int w = 0; w < 2; ++w) {
+        ext[w][0] = (hs[w] - 1) * a.xs[w][1] + D;
+        ext[w][1] = (hs[w] - 1) * a.os[w][1] + D;
+    }
+    const long total = (long)B * n;
+    const int size = dt == CSA_DT_F32 ? 4 : 2;
+    for (int w = 0; w < 2; ++w) {
+        if (!hs[w]) continue;
+        REQUIRE(xs[w] == os[w] || apart(xs[w], a.xs[w][0], ext[w][0], os[w], a.os[w][0], ext[w][1], total, size),
+                "%s: the output of %s overlaps it", name, w ? "y" : "x");
+        if (!hs[1 - w]) continue;
+        REQUIRE(apart(os[w], a.os[w][0], ext[w][1], xs[1 - w], a.xs[1 - w][0], ext[1 - w][0], total, size) &&
+                    apart(os[w], a.os[w][0], ext[w][1], os[1 - w], a.os[1 - w][0], ext[1 - w][1], total, size),
+                "%s: the output of %s overlaps the other tensor", name, w ? "y" : "x");
+    }
     // frequencies as 64-bit fractions of a turn (whole turns drop out)
     const long double inv_two_pi = 0.159154943091895335768883763372514362L;
     for (int j = 0; j < d_rot / 2; ++j) {

@@ -53,7 +53,7 @@ __global__ void __launch_bounds__(kThreads) weights_simt_kernel(WeightsArgs a) {
     for (int r = warp; r < a.n_q * a.H; r += kWarps) {
         const int qi = r / a.H;
         const int t = a.q_pos ? a.q_pos[(size_t)b * a.n_q + qi] : qi;
-        const int vis = t < 0 ? 0 : min((int)(((unsigned)t + 1u) / (unsigned)a.m), ne);
+        const int vis = t < 0 ? 0 : (int)min(((unsigned)t + 1u) / (unsigned)a.m, (unsigned)ne);
         const size_t row = (size_t)b * a.n_q * a.H + r;
         const float lse = a.lse[row];
         if (!(lse > -INFINITY) && lse == lse) continue;      // an empty row: no weight
@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(kMmaThreads) weights_mma_kernel(WeightsArgs a,
             if (c < cols) {
                 const int qi = c / a.H;
                 const int t = a.q_pos ? a.q_pos[(size_t)b * a.n_q + qi] : qi;
-                vis = t < 0 ? 0 : min((int)(((unsigned)t + 1u) / (unsigned)a.m), ne);
+                vis = t < 0 ? 0 : (int)min(((unsigned)t + 1u) / (unsigned)a.m, (unsigned)ne);
                 l = a.lse[(size_t)b * cols + c] * kLog2e;
                 if (l == -INFINITY) vis = 0;          // an empty row adds nothing
             }

@@ -59,7 +59,7 @@ struct __align__(16) Ctrl {
     uint64_t kfull[kKBufs], kfree[kKBufs];
     uint64_t s_full[kBufs], s_free[kBufs];         // scores, and the columns' lse and reach
     uint64_t x_full[kXs];
-    uint64_t fin;
+    uint64_t fin, stall_bar;     // (stall_bar: a barrier that nothing completes, for tests)
     uint32_t tmem_base;
     int abort;
 };
@@ -74,6 +74,7 @@ struct TcWeights {
     float sl2;
     uint32_t* err;
     uint64_t wait_ns;
+    int stall;                   // test hook: the MMA warp waits on stall_bar first
 };
 
 __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* err,
@@ -203,6 +204,7 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         }
         for (int i = 0; i < kXs; ++i) mbar_init(&ctl->x_full[i], kSumWarps - 4);
         mbar_init(&ctl->fin, 1);
+        mbar_init(&ctl->stall_bar, 1);
         // a CTA started after another one timed out does no work
         ctl->abort = (*reinterpret_cast<volatile uint32_t*>(p.err) != 0u) ? 1 : 0;
         fence_barrier_init();
@@ -299,7 +301,7 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             for (int e = 0; e < 2; ++e) {
                 const float l = -col.lse[e] * kLog2e;
                 const unsigned n = (unsigned)col.pos[e] + 1u;
-                const int vis = (col.pos[e] < 0 || l == INFINITY) ? 0 : min((int)(p.mshift >= 0 ? n >> p.mshift : n / (unsigned)a.m), col.ne);
+                const int vis = (col.pos[e] < 0 || l == INFINITY) ? 0 : (int)min(p.mshift >= 0 ? n >> p.mshift : n / (unsigned)a.m, (unsigned)col.ne);
                 ctl->nlse[sl][64 * cw + 32 * e + lane] = l;
                 ctl->vis[sl][64 * cw + 32 * e + lane] = vis;
                 const int low = __reduce_min_sync(0xffffffffu, vis), high = __reduce_max_sync(0xffffffffu, vis);
@@ -376,7 +378,7 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         // ------------------------------------------------------------ z^T = K.Q^T
         const uint64_t kd0 = sw128_desc(smem_u32(sK), 16, 1024), qd0 = sw128_desc(smem_u32(sQ), 16, 1024);
         int k = 0, L = 0;
-        bool ok = true;
+        bool ok = !p.stall || wait(&ctl->stall_bar, 0);
         for (Item t = first_live(); t.i < p.items && ok; next_live(t)) {
             const int kb = k % kKBufs;
             ok = wait(&ctl->kfull[kb], (k / kKBufs) & 1);
@@ -561,6 +563,7 @@ cudaError_t launch_entry_weights_tc(const WeightsArgs& a, uint32_t* err, cudaStr
     p.sl2 = a.scale * kLog2e;
     p.err = err;
     p.wait_ns = wait_limit_ns();
+    p.stall = take_stall();
     cudaError_t e = cudaFuncSetAttribute(weights_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
     if (e != cudaSuccess) return e;
     weights_tc_kernel<<<(unsigned)grid, kThreads, kSmem, s>>>(tm_k, tm_q, p);

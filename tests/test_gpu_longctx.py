@@ -451,6 +451,122 @@ def test_side_stream_and_captured_graphs():
         assert all(torch.equal(x, y) for x, y in zip(graphs[1][1], want_b))
 
 
+def test_positions_at_the_end_of_the_range():
+    # t + 1 passes 2^31 - 1: every entry is visible (m = 1)
+    last = 2 ** 31 - 1
+    for dt, H, D in ((BF, 64, 128), (BF, 16, 64), (F32, 8, 64)):
+        a = prefix_case(61, dt, 2, 1, H, D, 200, 10, 0, m=1)
+        a["q_pos"], a["n_entries"] = i32([[last], [last - 1]]), i32([210, 205])
+        check_prefix(a, dt)
+        w = weights_case(62, dt, 2, 1, H, D, 150, m=1)
+        w["q_pos"] = i32([[last], [last - 1]])
+        check_weights(w)
+
+
+@pytest.mark.parametrize("B,nq,H", [(310, 1, 64), (157, 2, 128), (9400, 1, 64)])
+def test_prefix_with_more_units_than_ctas(B, nq, H):
+    # several units a CTA, whole and cut; sampled elements against the definition
+    a = prefix_case(63, BF, B, nq, H, 128, 140, 5, 9, m=4, void=(B // 2, B - 1))
+    out, lse = run_prefix(a)
+    for b in sorted({0, 1, B // 3, B // 2, B // 2 + 1, B - 2, B - 1}):
+        one = {k: (v[b:b + 1] if isinstance(v, torch.Tensor) and k != "kv_p" else v) for k, v in a.items()}
+        want, wl, bound, bl = ref.prefix_attention(one, BF, BF)
+        within(out[b:b + 1], want, bound, f"element {b}")
+        within(lse[b:b + 1], wl, bl, f"lse of element {b}")
+    o2, l2 = run_prefix(a)
+    assert torch.equal(out, o2) and torch.equal(lse, l2)
+
+
+def test_offsets_past_32_bits():
+    # caches and heads whose last rows lie more than 2^31 elements in
+    g, B, N = gen(64), 5, 4_000_000
+    kv = torch.zeros(B, N, 128, dtype=BF, device=DEV)
+    b = B - 1
+    kv[b, :300] = normal(g, BF, 300, 128)
+    kv[b, N - 300:] = normal(g, BF, 300, 128)
+    q = normal(g, BF, B, 1, 64, 128)
+    ne, pos = i32([0] * (B - 1) + [300]), i32([[2 ** 30]] * B)
+    raw, p0 = normal(g, BF, B, 4, 128), i32([0] * B)
+    a = dict(q=q, kv_p=normal(g, BF, 130, 128), kv_c=kv, m=4, kv_raw=raw, window=0, n_entries=(ne + 130).contiguous(),
+             raw_pos0=p0, raw_len=i32([4] * B), q_pos=pos)
+    out, lse = run_prefix(a)
+    one = dict(a, q=q[b:], kv_c=kv[b:, :300], kv_raw=raw[b:], n_entries=i32([430]), raw_pos0=p0[b:], raw_len=i32([4]),
+               q_pos=pos[b:])
+    want, wl, bound, bl = ref.prefix_attention(one, BF, BF)
+    within(out[b:], want, bound, "last element")
+    within(lse[b:], wl, bl, "last element's lse")
+    idx = torch.full((B, 300), -1, dtype=torch.int32, device=DEV)
+    idx[b] = torch.arange(N - 300, N, device=DEV)
+    w = api.entry_weights(q, kv, 1, lse, idx=idx, q_pos=pos)
+    ww, bound = ref.entry_weights(q[b:], kv[b:, N - 300:], 1, lse[b:], None, None, None, pos[b:])
+    within(w[b:, N - 300:], ww, bound, "last entries' weights")
+    assert float(w[:, :N - 300].abs().sum()) == 0
+    w = api.entry_weights(q, kv, 1, lse, n_entries=ne, q_pos=pos)
+    ww, bound = ref.entry_weights(q[b:], kv[b:, :300], 1, lse[b:], None, None, None, pos[b:])
+    within(w[b:, :300], ww, bound, "first entries' weights")
+    assert float(w[:b].abs().sum()) == 0 and float(w[b, 300:].abs().sum()) == 0
+    del kv, a
+    freqs, _ = api.rope_freqs(64)
+    big = torch.zeros(1, 70000, 64, 512, dtype=BF, device=DEV)
+    big[0, -3:] = normal(g, BF, 3, 64, 512)
+    got, _ = api.rope(big, freqs, pos=None, rot_offset=448)
+    tail, _ = api.rope(big[:, -3:].contiguous(), freqs, pos=i32([[69997, 69998, 69999]]), rot_offset=448)
+    assert torch.equal(got[0, -3:], tail[0])
+
+
+@pytest.mark.parametrize("B,nq,N,topk", [(1030, 1, 130, 0), (1100, 1, 70, 9), (3, 3, 900, 0), (2, 5, 600, 333)])
+def test_entry_weights_many_elements_and_steps(B, nq, N, topk):
+    # more elements than their counts are kept for, steps of 128 columns with a half one last
+    a = weights_case(65, BF, B, nq, 64, 128, N, topk=topk)
+    got = run_weights(a)
+    for b in sorted({0, 1, B // 2, B - 2, B - 1}):
+        one = {k: (v[b:b + 1] if isinstance(v, torch.Tensor) else v) for k, v in a.items()}
+        want, bound = ref.entry_weights(one["q"], one["kv"], a["m"], one["lse"], one["weight"], one["idx"],
+                                        one["n_entries"], one["q_pos"])
+        within(got[b:b + 1], want, bound, f"element {b}")
+    if not topk:
+        assert torch.equal(got, run_weights(a))
+
+
+def test_prefix_workspace():
+    a = prefix_case(66, BF, 3, 1, 64, 128, 900, 30, 100, m=4)
+    want = run_prefix(a)
+    need = api.load().hca_dense_attn_prefix_workspace(api.DT_BF16, 3, 1, 64, 128, 900, 30, 100)
+    assert need > 0
+    ws = torch.full((need + 64,), 0xFF, dtype=torch.uint8, device=DEV)     # (all NaN as fp32)
+    got = run_prefix(a, workspace=ws[:need])
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert bool((ws[need:] == 0xFF).all())
+    for bad in (ws[:need - 1], ws[1:need + 1]):
+        with pytest.raises(api.CsaError):
+            run_prefix(a, workspace=bad)
+    with pytest.raises(ValueError, match="CUDA"):
+        run_prefix(a, workspace=ws.cpu())
+    with pytest.raises(ValueError, match="contiguous"):
+        run_prefix(a, workspace=ws[::2])
+
+
+def test_timeouts_are_reported_and_the_next_call_runs_clean():
+    lib = api.load()
+    a, w = prefix_case(67, BF, 70, 1, 64, 128, 700, 30, 100, m=4), weights_case(68, BF, 3, 2, 64, 128, 500)
+    for run in (lambda: run_prefix(a)[0], lambda: run_weights(w)):
+        api.csa_check_device_error()
+        want = run()
+        torch.cuda.synchronize()
+        assert lib.csa_debug_set_wait_limit(2_000_000, 1) == api.CSA_OK       # 2 ms, stall the next launch
+        try:
+            run()
+            with pytest.raises(api.CsaError) as ei:
+                api.csa_check_device_error(clear=True)
+            assert ei.value.status == api.CSA_ERR_TIMEOUT
+        finally:
+            assert lib.csa_debug_set_wait_limit(0, 0) == api.CSA_OK
+        api.csa_check_device_error()
+        assert torch.equal(run(), want)
+        torch.cuda.synchronize()
+        api.csa_check_device_error()
+
+
 def test_stream_argument():
     a = prefix_case(51, BF, 2, 1, 64, 128, 300, 10, 50, m=4)
     want = run_prefix(a)

@@ -58,6 +58,56 @@ def test_rope_validation(lib):
         assert call(*changed(ok, **change)) == OK, change
 
 
+def test_rope_refuses_tensors_that_overlap(lib):
+    f = (ctypes.c_double * 32)(*([0.5] * 32))
+    p = lambda v: ctypes.c_void_p(0x100000 + v)  # noqa: E731
+    one = 4 * 2 * 64 * 2                                   # bytes of [1, 4, 2, 64] bf16
+    far = p(1 << 20)
+
+    def call(x, xo, y, yo, xs=None, ys=None, n=4):
+        return lib.csa_rope(x, xo, 2, xs, y, yo, 2, ys, 1, 1, n, 64, 32, 0, 1, f, 1.0, None, 0, 1, 0, None)
+
+    def launched(*a, **kw):                                # accepted: it gets as far as the launch
+        assert lib.csa_debug_inject_launch_error(719) == OK
+        return call(*a, **kw) == api.CSA_ERR_CUDA
+
+    assert call(p(0), p(one // 2), p(8 * one), p(9 * one)) == INV      # x's output inside x
+    assert call(p(0), p(one), p(0), p(one)) == INV                     # one output for both
+    assert call(p(0), p(0), p(0), p(0)) == INV                         # the same tensor twice, in place
+    assert call(p(0), p(one), p(one), p(2 * one)) == INV               # x's output is y
+    assert call(p(0), p(one), p(4 * one), p(0)) == INV                 # y's output is x
+    assert launched(p(0), p(one), p(0), p(2 * one))                    # one input, two outputs
+    assert launched(p(0), p(0), p(one), p(one))                        # neighbours, in place
+    # heads 0-1 and 2-3 of one [1, 4, 5, 64] buffer, in place; heads 1-2 overlap the first
+    fused = st(320, 64, 320, 64)
+    assert launched(p(0), p(0), p(256), p(256), fused, fused)
+    assert call(p(0), p(0), p(128), p(128), fused, fused) == INV
+    assert call(p(0), p(0), p(256), p(256), fused, st(256, 64, 256, 64)) == INV      # other token strides
+    assert launched(p(0), far, p(256), p(2 << 20), st(320, 64, 128, 64), st(320, 64, 128, 64))
+    assert call(p(0), p(0), p(128), p(128), fused, fused, n=1) == INV
+    assert launched(p(0), p(0), p(256), p(256), fused, fused, n=1)
+
+
+def test_binding_refuses_other_devices(monkeypatch):
+    class Other:                                           # a tensor of device 1, as the binding sees it
+        is_cuda, device, dtype, shape = True, "cuda:1", torch.float32, torch.Size((2, 4))
+
+        def get_device(self):
+            return 1
+
+    monkeypatch.setattr(api, "_device", lambda: 0)
+    with pytest.raises(ValueError, match="current device is cuda:0"):
+        api._same_device(Other())
+    with pytest.raises(ValueError, match="on cuda:1, the first tensor on cuda:0"):
+        api._shape(Other(), (2, 4), "idx", 0)
+    with pytest.raises(ValueError, match="on cuda:1, the first tensor on the host"):
+        api._shape(Other(), (2, 4), "idx", -1)
+    with pytest.raises(ValueError, match="CUDA tensors"):
+        api._shape(torch.zeros(2, 4), (2, 4), "idx", 0)
+    with pytest.raises(ValueError, match="CUDA tensors"):
+        api._rope_tensor(torch.zeros(1, 2, 1, 8), torch.zeros(1, 2, 1, 8), 1, 2, 8, torch.float32, "y", 0)
+
+
 def test_rope_freqs(lib):
     f, s = api.rope_freqs(64)
     assert s == 1.0
