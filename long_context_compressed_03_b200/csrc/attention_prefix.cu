@@ -146,14 +146,16 @@ template <int G>
 __device__ __forceinline__ void fill_geometry(const PrefixParams& p, int c, int n_cta, int u0, int n, Geo* geo,
                                               RowRec* rows) {
     constexpr int H = kRows / G;
-    for (int i = threadIdx.x; i < n * G; i += kThreads) {
+    // (by warps that have nothing else to set up; a row's arrays are read at once)
+    constexpr int kFirst = kSoftWarp0 * 32, kStep = kThreads - kFirst;
+    for (int i = (int)threadIdx.x - kFirst; i >= 0 && i < n * G; i += kStep) {
         const int row = u0 * G + i;
         RowRec r{};
         if (row < p.R) {
             r.b = row / p.a.n_q;
             const int t = p.a.q_pos ? __ldg(p.a.q_pos + row) : row - r.b * p.a.n_q;
+            const RowKeys k = row_keys(p.a, r.b, t);
             if (t >= 0) {
-                const RowKeys k = row_keys(p.a, r.b, t);
                 r.on = 1;
                 r.vis = k.n_comp;
                 r.win_lo = k.win_lo;
@@ -163,7 +165,7 @@ __device__ __forceinline__ void fill_geometry(const PrefixParams& p, int c, int 
         rows[i] = r;
     }
     __syncthreads();
-    for (int k = threadIdx.x; k < n; k += kThreads) {
+    for (int k = (int)threadIdx.x - kFirst; k >= 0 && k < n; k += kStep) {
         Geo g{};
         int lo = p.a.N_p, on = 0;
 #pragma unroll
@@ -302,6 +304,8 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     const int u0 = first_unit(p, c, n_cta), u1 = end_unit(p, c, n_cta);
 
     if (threadIdx.x == 0) {
+        // a CTA started after another one timed out does no work
+        const bool dead = *reinterpret_cast<volatile uint32_t*>(p.err) != 0u;
         mbar_init(&ctl->bar_q, 1);
         mbar_init(&ctl->q_free, 1);
         for (int i = 0; i < kStages; ++i) {
@@ -322,8 +326,6 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         mbar_init(&ctl->stall_bar, 1);
         ctl->over[0] = ctl->over[1] = ctl->over[2] = 0;
         fence_barrier_init();
-        // a CTA started after another one timed out does no work
-        const bool dead = *reinterpret_cast<volatile uint32_t*>(p.err) != 0u;
         ctl->abort = dead;
         ctl->q_ahead = !dead;
     }
