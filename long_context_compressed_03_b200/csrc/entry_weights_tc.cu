@@ -10,8 +10,8 @@
 // tiles past the elements' ends come last and cost nothing.
 // Roles (24 warps): warp 0 loads Q and the entries' tiles (TMA); warps 1-2 stage
 // the columns' lse and reach; warps 3-6 gather listed entries row by row
-// (cp.async); warp 7 issues the MMAs; warps 8-23 take the four quarters of a
-// step's columns.  (One group of warps for all loads took 1800 cycles a step, most
+// (cp.async); warp 7 issues the MMAs; warps 8-23 add the weights, four threads a
+// key.  (One group of warps for all loads took 1800 cycles a step, most
 // of it waiting for its own instructions and lse, and 8 warps for the sums left
 // tensor-memory loads and exponentials one after the other: 47 us for 64 query
 // rows over 16384 entries.)
@@ -171,6 +171,8 @@ __device__ __forceinline__ void next_item(const TcWeights& p, const int* ne, Ite
     look(p, ne, t);
 }
 
+// kOne: items of one step.
+template <bool kOne>
 __global__ void __launch_bounds__(kThreads, 1)
 weights_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_q,
                   const __grid_constant__ TcWeights p) {
@@ -200,9 +202,9 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         }
         for (int i = 0; i < kBufs; ++i) {
             mbar_init(&ctl->s_full[i], 1 + kColWarps);
-            mbar_init(&ctl->s_free[i], kSumWarps);
+            mbar_init(&ctl->s_free[i], kOne ? kSumWarps / 2 : kSumWarps);
         }
-        for (int i = 0; i < kXs; ++i) mbar_init(&ctl->x_full[i], kSumWarps - 4);
+        for (int i = 0; i < kXs; ++i) mbar_init(&ctl->x_full[i], kOne ? 4 : kSumWarps - 4);
         mbar_init(&ctl->fin, 1);
         mbar_init(&ctl->stall_bar, 1);
         // a CTA started after another one timed out does no work
@@ -412,7 +414,13 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         __syncwarp();
     } else {
         // ------------------------------------------------------------ weights and sums
-        const int h = (warp - kSumWarp0) >> 2;               // which quarter of a step's columns
+        // Four threads a key.  Items of several steps: each takes a quarter of every
+        // step's columns.  Items of one step: every other item, half of its columns
+        // (the waits and meetings an item costs overlap the other half's work:
+        // decode of 16 x 8192 entries takes 9.3 us, in quarters 10.3).
+        const int h = (warp - kSumWarp0) >> 2;
+        constexpr int share = kOne ? 2 : kQuarters;
+        const int part_of = h & (share - 1);
         const int r = (warp & 3) * 32 + lane;                // key of the item
         const uint32_t my = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint64_t sl2 = f2_pack(p.sl2, p.sl2);
@@ -424,7 +432,7 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             int s = a.idx ? (j < a.topk ? __ldg(a.idx + (size_t)t.b * a.topk + j) : -1) : j;
             if (s < 0 || s >= a.N_cap) s = -1;
             *had = 0.0f;
-            if (h == 0 && !a.idx && s >= 0 && a.in) *had = a.in[(size_t)t.b * a.N_cap + s];
+            if (part_of == 0 && !a.idx && s >= 0 && a.in) *had = a.in[(size_t)t.b * a.N_cap + s];
             return s;
         };
         Item tn = first_item(p, ctl->ne);
@@ -441,51 +449,60 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 if (h == 0 && !a.idx && s >= 0) *dst = had;
                 continue;
             }
+            if (kOne && (k & 1) != (h >> 1)) {
+                ++k;
+                ++L;
+                continue;
+            }
             float sum = 0.0f;
             for (int st = 0; st < p.steps; ++st, ++L) {
                 const int buf = L % kBufs;
-                // this quarter's columns of the step: 32, or a quarter of what the last step has
-                const int n = min(kCols, (p.cols - st * kCols + 63) & ~63) / kQuarters, c0 = n * h;
+                // this thread's columns of the step: a quarter or half of 128 or 64
+                const int n = min(kCols, (p.cols - st * kCols + 63) & ~63) / share, c0 = n * part_of;
                 // every wait is warp-collective: the TMEM accesses below are .sync.aligned
                 ok = wait(&ctl->s_full[buf], (L / kBufs) & 1);
                 if (!ok) break;
                 tc_fence_after();
-                // columns of one query row (or rows that see the same): one test for all
-                const int same = ctl->low[buf][c0 >> 5];
-                float part = 0.0f;
-                if (n == 32 && same >= 0) {
-                    part = sum_columns<32>(my + buf * kCols + c0, &ctl->nlse[buf][c0], sl2);
-                } else if (same >= 0) {
-                    part = sum_columns<16>(my + buf * kCols + c0, &ctl->nlse[buf][c0], sl2);
-                } else {
 #pragma unroll 1
-                    for (int c = c0; c < c0 + n; c += 16) {
-                        float z[16];
-                        tmem_ld16(my + buf * kCols + c, z);
+                for (int c = c0; c < (kOne ? c0 + n : c0 + 1); c += 32) {
+                    // columns of one query row (or rows that see the same): one test for all
+                    const int same = ctl->low[buf][c >> 5];
+                    float part = 0.0f;
+                    if (n >= 32 && same >= 0) {
+                        part = sum_columns<32>(my + buf * kCols + c, &ctl->nlse[buf][c], sl2);
+                    } else if (same >= 0) {
+                        part = sum_columns<16>(my + buf * kCols + c, &ctl->nlse[buf][c], sl2);
+                    } else {
+#pragma unroll 1
+                        for (int d = c; d < c + min(n, 32); d += 16) {
+                            float z[16];
+                            tmem_ld16(my + buf * kCols + d, z);
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const float w = ex2(fmaf(z[e], p.sl2, ctl->nlse[buf][c + e]));
-                            if (s < ctl->vis[buf][c + e]) part += w;
+                            for (int e = 0; e < 16; ++e) {
+                                const float w = ex2(fmaf(z[e], p.sl2, ctl->nlse[buf][d + e]));
+                                if (s < ctl->vis[buf][d + e]) part += w;
+                            }
                         }
                     }
+                    if (same < 0 || s < same) sum += part;   // (what a key may not add may be NaN)
                 }
-                if (same < 0 || s < same) sum += part;       // (what a key may not add may be NaN)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ctl->s_free[buf]);
             }
             if (!ok) break;
-            // the quarters' sums meet.  (The others are at most kBufs steps, so kBufs
+            // the shares' sums meet.  (The others are at most kBufs steps, so kBufs
             // items, ahead: their slot of xs has been read.)
-            if (h > 0) {
-                ctl->xs[k % kXs][h - 1][r] = sum;
+            if (part_of > 0) {
+                ctl->xs[k % kXs][part_of - 1][r] = sum;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ctl->x_full[k % kXs]);
             } else {
                 ok = wait(&ctl->x_full[k % kXs], (k / kXs) & 1);
                 if (!ok) break;
 #pragma unroll
-                for (int q = 0; q < kQuarters - 1; ++q) sum += ctl->xs[k % kXs][q][r];
+                for (int q = 0; q < kQuarters - 1; ++q)
+                    if (q < share - 1) sum += ctl->xs[k % kXs][q][r];
                 if (s >= 0) {
                     // (an entry listed twice receives its weight twice: equal terms, any order)
                     if (a.idx) atomicAdd(dst, sum);
@@ -564,9 +581,10 @@ cudaError_t launch_entry_weights_tc(const WeightsArgs& a, uint32_t* err, cudaStr
     p.err = err;
     p.wait_ns = wait_limit_ns();
     p.stall = take_stall();
-    cudaError_t e = cudaFuncSetAttribute(weights_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    const auto kern = p.steps == 1 ? weights_tc_kernel<true> : weights_tc_kernel<false>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
     if (e != cudaSuccess) return e;
-    weights_tc_kernel<<<(unsigned)grid, kThreads, kSmem, s>>>(tm_k, tm_q, p);
+    kern<<<(unsigned)grid, kThreads, kSmem, s>>>(tm_k, tm_q, p);
     count_launch();
     return cudaGetLastError();
 }
