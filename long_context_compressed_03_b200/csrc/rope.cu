@@ -77,9 +77,9 @@ __device__ __forceinline__ uint4 pack(const float* f, __nv_bfloat16) {
 // down the rows.  Its next kDepth - 1 rows are on their way to its own slots of
 // shared memory (cp.async, no barrier), the first of them while the angles are made.
 // Bound by HBM: every byte is read and written once.  2 x 8192 tokens of 65 x 128
-// bf16 take 90 us, 92% of a plain copy's rate; in batches of four rows through
+// bf16 take 87 us, 96% of a plain copy's rate; in batches of four rows through
 // registers, which drain before the next is asked for, 114 us.  Depths of 3, 6 and 8
-// took 94, 93 and 94 us.
+// took 4, 3 and 4 us more.
 constexpr int kDepth = 4;
 template <bool HALF>
 __host__ __device__ constexpr size_t ring_bytes() { return (size_t)kDepth * kThreads * (HALF ? 32 : 16); }
@@ -89,73 +89,133 @@ __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
                  ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
 }
 
+// How a call is cut: tokens a CTA; rows a CTA of one token, and such CTAs a token; items
+// a row; rows a step of the CTA's threads.  The divisors come with their reciprocals
+// (the calls of a few us wait for every division).
+struct RopeGrid {
+    int tpb, rpb, chunks, ipr, row_step;
+    float inv_rot, inv_pass, inv_h[2], inv_step;
+};
+// x / d for 0 <= x < 2^20, given 1 / d
+__device__ __forceinline__ int quot(int x, float inv) { return (int)(((float)x + 0.5f) * inv); }
+
 template <typename T, bool HALF>
 __global__ void __launch_bounds__(kThreads, 4)
-rope_vec_kernel(const __grid_constant__ RopeArgs a, int tpb, int rpb, int chunks, int ipr) {
+rope_vec_kernel(const __grid_constant__ RopeArgs a, const __grid_constant__ RopeGrid g) {
     constexpr int V = 16 / sizeof(T);
     extern __shared__ __align__(16) uint8_t smem[];
     float2* cs = reinterpret_cast<float2*>(smem + ring_bytes<HALF>());
     const int half = a.d_rot / 2;
+    const int tpb = g.tpb, ipr = g.ipr, row_step = g.row_step;
     int* ok = reinterpret_cast<int*>(cs + (size_t)tpb * half);
     const long total = (long)a.B * a.n;
-    const long tok0 = (long)(blockIdx.x / chunks) * tpb;
-    const int r0 = (int)(blockIdx.x % chunks) * rpb;
+    const int tile = g.chunks == 1 ? (int)blockIdx.x : (int)(blockIdx.x / g.chunks);
+    const long tok0 = (long)tile * tpb;
+    const int r0 = ((int)blockIdx.x - tile * g.chunks) * g.rpb;
     const int n_tok = (int)min((long)tpb, total - tok0);
-    const int R = min(a.H[0] + a.H[1] - r0, rpb);
-    const int rot_items = (HALF ? half : a.d_rot) / V;
-    const int it = threadIdx.x % ipr, row_step = kThreads / ipr;
-    // the item's element offset in a row (HALF: of the first of its two vectors)
-    const bool rot = it < rot_items;
-    int e0 = a.off + it * V;
-    if (!rot) {
-        e0 = (it - rot_items) * V;
-        if (e0 >= a.off) e0 += a.d_rot;
+    const int R = min(a.H[0] + a.H[1] - r0, g.rpb);
+    const int rot_items = (HALF ? half : a.d_rot) / V, pass_items = ipr - rot_items;
+    // Rotated items to the first threads, the others to the rest: a warp of both kinds
+    // would run the rotation for a third of its lanes.  (So mapped, and with every row's
+    // offset computed anew, instruction issue was 79% busy: 90 us for the call above, 97
+    // where its tensors' addresses collide in DRAM.)
+    const bool rot = (int)threadIdx.x < row_step * rot_items;
+    int it, rr0;                                             // the thread's item, and its first row
+    if (rot) {
+        rr0 = quot(threadIdx.x, g.inv_rot);
+        it = threadIdx.x - rr0 * rot_items;
+    } else {
+        const int u = threadIdx.x - row_step * rot_items;
+        rr0 = pass_items ? quot(u, g.inv_pass) : row_step;
+        it = u - rr0 * pass_items;
     }
+    // the item's element offset in a row (HALF: of the first of its two vectors)
+    int e0 = it * V;
+    if (rot) e0 += a.off;
+    else if (e0 >= a.off) e0 += a.d_rot;
     const int pair0 = HALF ? it * V : it * (V / 2);
-    const int rows = (int)threadIdx.x < row_step * ipr ? n_tok * R : 0;    // (the last threads may have no item)
-    // the thread's rows, row_step apart: (token, row of it) of the next to load / to store
-    const int dt = row_step / R, dr = row_step - dt * R;
-    const int rr0 = threadIdx.x / ipr;
-    int lt = rr0 / R, lr = rr0 - lt * R, st = lt, sr = lr;
-    const auto step = [&](int& t, int& r) {
-        t += dt;
-        r += dr;
-        if (r >= R) {
-            r -= R;
-            ++t;
+    // The CTA's rows: the hx x heads of its tokens, then their hy y heads.  A thread's
+    // rows are row_step apart.
+    const int hx = min(max(a.H[0] - r0, 0), R), hy = R - hx;
+    const int nx = n_tok * hx, rows = n_tok * R;
+    struct Rows {                // walks them
+        const T* p;
+        long inc, wrap;          // to the next row; and, past a token's last row, back to the next token's
+        int v, r, t, h, dr, dt;  // row, its head and token; heads a token; steps of r and t
+    };
+    const auto row = [&](Rows& w, int v) {
+        const bool y = v >= nx;
+        w.v = v;
+        if (y) v -= nx;
+        if (tpb == 1) {          // (one token: no row is past its last)
+            w.h = 1 << 30;
+            w.t = w.dt = 0;
+            w.r = v;
+            w.dr = row_step;
+            return;
+        }
+        w.h = y ? hy : hx;
+        w.t = quot(v, g.inv_h[y]);
+        w.r = v - w.t * w.h;
+        w.dt = quot(row_step, g.inv_h[y]);
+        w.dr = row_step - w.dt * w.h;
+    };
+    const auto aim = [&](Rows& w, const void* const* ptr, const long(*sd)[2]) {
+        const bool y = w.v >= nx;
+        const long s0 = sd[y][0], s1 = sd[y][1];
+        w.inc = w.dt * s0 + w.dr * s1;
+        w.wrap = s0 - w.h * s1;
+        const int h0 = y ? max(r0 - a.H[0], 0) : r0;
+        w.p = static_cast<const T*>(ptr[y]) + (tok0 + w.t) * s0 + (h0 + w.r) * s1 + e0;
+    };
+    const auto step = [&](Rows& w, const void* const* ptr, const long(*sd)[2]) {
+        const bool x = w.v < nx;
+        w.v += row_step;
+        if (x && w.v >= nx) {    // from the x heads to the y heads
+            row(w, w.v);
+            aim(w, ptr, sd);
+            return;
+        }
+        w.t += w.dt;
+        w.r += w.dr;
+        w.p += w.inc;
+        if (w.r >= w.h) {
+            w.r -= w.h;
+            ++w.t;
+            w.p += w.wrap;
         }
     };
-    // where a row's item is in the input / the output
-    const auto at = [&](int t, int r, const void* const* ptr, const long(*sd)[2]) {
-        const int h0 = r0 + r;
-        const int w = h0 >= a.H[0];
-        return static_cast<const T*>(ptr[w]) + (tok0 + t) * sd[w][0] + (w ? h0 - a.H[0] : h0) * sd[w][1] + e0;
-    };
+    Rows in, out;
+    row(in, rr0);
+    out = in;
+    aim(in, a.x, a.xs);
     uint4* ring = reinterpret_cast<uint4*>(smem) + threadIdx.x;          // [kDepth][1 or 2][kThreads]
     constexpr int kSlot = (HALF ? 2 : 1) * kThreads;
-    const int count = rows > rr0 ? (rows - rr0 + row_step - 1) / row_step : 0;
-    int loaded = 0;
+    int left = rr0 < row_step && rows > rr0 ? quot(rows - rr0 + row_step - 1, g.inv_step) : 0;
+    int count = left, slot = 0;
     const auto load = [&]() {
-        if (loaded < count) {
-            const T* p = at(lt, lr, a.x, a.xs);
-            uint4* d = ring + loaded % kDepth * kSlot;
-            cp_async16(d, p);
-            if (HALF && rot) cp_async16(d + kThreads, p + half);
-            step(lt, lr);
-            ++loaded;
+        if (left > 0) {
+            uint4* d = ring + slot * kSlot;
+            cp_async16(d, in.p);
+            if (HALF && rot) cp_async16(d + kThreads, in.p + half);
+            step(in, a.x, a.xs);
+            --left;
         }
+        slot = (slot + 1) % kDepth;
         asm volatile("cp.async.commit_group;" ::: "memory");             // (one a step, if empty)
     };
 #pragma unroll
     for (int i = 0; i < kDepth - 1; ++i) load();
     fill_angles(a, tok0, n_tok, cs, ok);
-    for (int k = 0; k < count; ++k) {
+    aim(out, a.out, a.os);
+    for (; count > 0; --count) {
         asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 2) : "memory");
-        const uint4* d = ring + k % kDepth * kSlot;
+        const uint4* d = ring + (slot + 1) % kDepth * kSlot;
         uint4 v = d[0], w = make_uint4(0, 0, 0, 0);
         if (HALF && rot) w = d[kThreads];
         load();                                              // (into the slot read a step ago)
-        T* p = const_cast<T*>(at(st, sr, a.out, a.os));
+        const int st = out.t;
+        T* p = const_cast<T*>(out.p);
         if (rot && ok[st]) {
             const float2* c = cs + st * half + pair0;
             float x[V], y[V];
@@ -183,7 +243,7 @@ rope_vec_kernel(const __grid_constant__ RopeArgs a, int tpb, int rpb, int chunks
         }
         *reinterpret_cast<uint4*>(p) = v;
         if (HALF && rot) *reinterpret_cast<uint4*>(p + half) = w;
-        step(st, sr);
+        step(out, a.out, a.os);
     }
 }
 
@@ -219,6 +279,9 @@ cudaError_t launch_vec(const RopeArgs& a, cudaStream_t s) {
         chunks = (R + want - 1) / want;
         rpb = (R + chunks - 1) / chunks;
     }
+    const auto inv = [](int d) { return d > 0 ? 1.0f / (float)d : 0.0f; };
+    const int rot_items = (a.interleaved ? a.d_rot : a.d_rot / 2) / V;
+    const RopeGrid g{tpb, rpb, chunks, ipr, step, inv(rot_items), inv(ipr - rot_items), {inv(a.H[0]), inv(a.H[1])}, inv(step)};
     const long blocks = (total + tpb - 1) / tpb * chunks;
     if (blocks > (1L << 31) - 1) return cudaErrorInvalidConfiguration;
     const size_t smem = (a.interleaved ? ring_bytes<false>() : ring_bytes<true>()) +
@@ -226,7 +289,7 @@ cudaError_t launch_vec(const RopeArgs& a, cudaStream_t s) {
     auto kern = a.interleaved ? rope_vec_kernel<T, false> : rope_vec_kernel<T, true>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    kern<<<(unsigned)blocks, kThreads, smem, s>>>(a, tpb, rpb, chunks, ipr);
+    kern<<<(unsigned)blocks, kThreads, smem, s>>>(a, g);
     count_launch();
     return cudaGetLastError();
 }
