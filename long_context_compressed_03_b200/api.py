@@ -532,8 +532,9 @@ def _rope_strides(x: torch.Tensor, out: torch.Tensor, name: str):
 
 
 def _rope_tensor(x: torch.Tensor | None, out: torch.Tensor | None, B: int, n: int, D: int, dt, name: str,
-                 dev: int = -1):
-    """(x, out, heads, strides) arguments of csa_rope for one tensor [B, n, H, D]."""
+                 dev: int = -1, fresh: bool = False):
+    """(x, out, heads, strides) arguments of csa_rope for one tensor [B, n, H, D]; ``fresh``:
+    out was just allocated for it (contiguous)."""
     if x is None:
         if out is not None:
             raise ValueError(f"an output for {name}, but no {name}")
@@ -543,11 +544,14 @@ def _rope_tensor(x: torch.Tensor | None, out: torch.Tensor | None, B: int, n: in
     sh = x.shape
     if len(sh) != 4 or sh[0] != B or sh[1] != n or sh[3] != D or x.dtype is not dt:
         raise ValueError(f"{name} must be [B, n, heads, D], of one shape and dtype with the other tensor")
-    if out.shape != sh or out.dtype is not dt:
+    if not fresh and (out.shape != sh or out.dtype is not dt):
         raise ValueError(f"the output of {name} must have its shape and dtype")
-    for t in (x, out):
-        if dev < 0 or t.get_device() != dev:
-            _refuse_device(t, name, dev)
+    if dev < 0 or x.get_device() != dev:
+        _refuse_device(x, name, dev)
+    if fresh and x.is_contiguous():
+        return x.data_ptr(), out.data_ptr(), sh[2], None
+    if out.get_device() != dev:
+        _refuse_device(out, name, dev)
     xp, op = x.data_ptr(), out.data_ptr()
     if x.is_contiguous() and out.is_contiguous():
         size = x.numel() * x.element_size()
@@ -566,14 +570,20 @@ def csa_rope(x: torch.Tensor, x_out: torch.Tensor, freqs: torch.Tensor,
     be the inputs.  ``freqs``: float64 host tensor [d_rot / 2]; ``pos`` [B, n] int32, or
     token j sits at pos0 + j * pos_step.  Views of a larger tensor are taken as long as
     their channels are contiguous and their elements n tokens apart."""
+    _rope(x, x_out, freqs, y, y_out, pos, rot_offset, interleaved, scale, pos0, pos_step, transpose,
+          stream, False)
+
+
+def _rope(x, x_out, freqs, y, y_out, pos, rot_offset, interleaved, scale, pos0, pos_step, transpose,
+          stream, fresh):
     if x.dim() != 4:
         raise ValueError("x must be [B, n, heads, D]")
     if freqs.dtype is not torch.float64 or freqs.is_cuda or freqs.dim() != 1 or not freqs.is_contiguous():
         raise ValueError("freqs must be a contiguous float64 host tensor [d_rot / 2]")
     B, n, _, D = x.shape
-    dev = _same_device(x)
-    xa, xo, H, xs = _rope_tensor(x, x_out, B, n, D, x.dtype, "x", dev)
-    ya, yo, Hy, ys = _rope_tensor(y, y_out, B, n, D, x.dtype, "y", dev)
+    dev, dt = _same_device(x), x.dtype
+    xa, xo, H, xs = _rope_tensor(x, x_out, B, n, D, dt, "x", dev, fresh)
+    ya, yo, Hy, ys = _rope_tensor(y, y_out, B, n, D, dt, "y", dev, fresh)
     _check(load().csa_rope(xa, xo, H, xs, ya, yo, Hy, ys, _dt(x), B, n, D, 2 * freqs.numel(),
                            rot_offset, interleaved, freqs.data_ptr(), scale,
                            _shape(pos, (B, n), "pos", dev, torch.int32), pos0, pos_step, transpose,
@@ -592,26 +602,36 @@ def hca_dense_attn_prefix(q: torch.Tensor, kv_p: torch.Tensor, kv_c: torch.Tenso
     """hca_dense_attn over entries kv_p [N_p, D] (shared by the batch), then kv_c
     [B, N_cap, D].  ``workspace``: a CUDA tensor of hca_dense_attn_prefix_workspace(...)
     bytes; None takes one from torch's allocator, on the stream the call runs on."""
+    _prefix(q, kv_p, kv_c, m, kv_raw, window, out, lse_out, n_entries, raw_pos0, raw_len, q_pos,
+            softmax_scale, workspace, stream)
+
+
+def _prefix(q, kv_p, kv_c, m, kv_raw, window, out, lse_out, n_entries, raw_pos0, raw_len, q_pos,
+            softmax_scale, workspace, stream, new_out=None, new_lse=None):
+    """``new_out`` (and ``new_lse``): just allocated like q, instead of out and lse_out."""
     B, n_q, H, D = q.shape
-    dev = _same_device(q)
-    if not (q.dtype is kv_p.dtype is kv_c.dtype is kv_raw.dtype is out.dtype):
+    dev, dtype = _same_device(q), q.dtype
+    if not (dtype is kv_p.dtype is kv_c.dtype is kv_raw.dtype) or (out is not None and out.dtype is not dtype):
         raise ValueError("q, kv_p, kv_c, kv_raw and out must share one dtype")
     N_p, N_cap, L = kv_p.shape[0], kv_c.shape[1], kv_raw.shape[1]
     dt, i32 = _dt(q), torch.int32
-    lib = load()
-    if workspace is None and dev >= 0:
+    args = (_shape(q, q.shape, "q", dev), dt, B, n_q, H, D, _shape(kv_p, (N_p, D), "kv_p", dev), N_p,
+            _shape(kv_c, (B, N_cap, D), "kv_c", dev), N_cap, _shape(n_entries, (B,), "n_entries", dev, i32),
+            m, _shape(kv_raw, (B, L, D), "kv_raw", dev), L, _shape(raw_pos0, (B,), "raw_pos0", dev, i32),
+            _shape(raw_len, (B,), "raw_len", dev, i32), window, _shape(q_pos, (B, n_q), "q_pos", dev, i32),
+            softmax_scale)
+    if new_out is not None:
+        outs = (new_out.data_ptr(), None if new_lse is None else new_lse.data_ptr())
+    else:
+        outs = (_shape(out, (B, n_q, H, D), "out", dev), _shape(lse_out, (B, n_q, H), "lse_out", dev, torch.float32))
+    if workspace is not None:
+        wb = workspace.numel() * workspace.element_size()
+        ws = _shape(workspace, workspace.shape, "workspace", dev)
+    else:
         wb = _prefix_workspace(dt, B, n_q, H, D, N_p, N_cap, window)
         workspace = _scratch(wb, q.device, stream) if wb else None
-    else:
-        wb = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    ws = None if workspace is None else _shape(workspace, workspace.shape, "workspace", dev)
-    _check(lib.hca_dense_attn_prefix(
-        _shape(q, q.shape, "q", dev), dt, B, n_q, H, D, _shape(kv_p, (N_p, D), "kv_p", dev), N_p,
-        _shape(kv_c, (B, N_cap, D), "kv_c", dev), N_cap, _shape(n_entries, (B,), "n_entries", dev, i32),
-        m, _shape(kv_raw, (B, L, D), "kv_raw", dev), L, _shape(raw_pos0, (B,), "raw_pos0", dev, i32),
-        _shape(raw_len, (B,), "raw_len", dev, i32), window, _shape(q_pos, (B, n_q), "q_pos", dev, i32),
-        softmax_scale, _shape(out, (B, n_q, H, D), "out", dev),
-        _shape(lse_out, (B, n_q, H), "lse_out", dev, torch.float32), ws, wb, _stream(stream)))
+        ws = workspace.data_ptr() if wb else None
+    _check(load().hca_dense_attn_prefix(*args, *outs, ws, wb, _stream(stream)))
 
 
 @functools.lru_cache(maxsize=1024)
@@ -638,20 +658,24 @@ def hca_entry_weights(q: torch.Tensor, kv_c: torch.Tensor, m: int, lse: torch.Te
     """weight_out [B, N_cap] = weight_in (or 0) + the weight that each visible (or listed:
     idx [B, topk]) entry of kv_c [B, N_cap, D] received from q [B, n_q, H, D], given the
     attention's lse [B, n_q, H]."""
+    B, N_cap, _ = kv_c.shape
+    out = _shape(weight_out, (B, N_cap), "weight_out", _same_device(q), torch.float32) \
+        if q.dtype is kv_c.dtype else None
+    _weights(q, kv_c, m, lse, out, weight_in, idx, n_entries, q_pos, softmax_scale, stream)
+
+
+def _weights(q, kv_c, m, lse, out, weight_in, idx, n_entries, q_pos, softmax_scale, stream):
     B, n_q, H, D = q.shape
-    dev = _same_device(q)
-    if q.dtype != kv_c.dtype:
+    dev, i32, f32 = _same_device(q), torch.int32, torch.float32
+    if q.dtype is not kv_c.dtype:
         raise ValueError("q and kv_c must share one dtype")
     N_cap = kv_c.shape[1]
     topk = 0 if idx is None else idx.shape[-1]
     _check(load().hca_entry_weights(
         _shape(q, q.shape, "q", dev), _dt(q), B, n_q, H, D, _shape(kv_c, (B, N_cap, D), "kv_c", dev), N_cap,
-        _shape(idx, (B, topk), "idx", dev, torch.int32), topk,
-        _shape(n_entries, (B,), "n_entries", dev, torch.int32), m,
-        _shape(q_pos, (B, n_q), "q_pos", dev, torch.int32), softmax_scale,
-        _shape(lse, (B, n_q, H), "lse", dev, torch.float32),
-        _shape(weight_in, (B, N_cap), "weight_in", dev, torch.float32),
-        _shape(weight_out, (B, N_cap), "weight_out", dev, torch.float32), _stream(stream)))
+        _shape(idx, (B, topk), "idx", dev, i32), topk, _shape(n_entries, (B,), "n_entries", dev, i32), m,
+        _shape(q_pos, (B, n_q), "q_pos", dev, i32), softmax_scale, _shape(lse, (B, n_q, H), "lse", dev, f32),
+        _shape(weight_in, (B, N_cap), "weight_in", dev, f32), out, _stream(stream)))
 
 
 def csa_evict(weight: torch.Tensor, budget: int, idx_out: torch.Tensor,
@@ -661,12 +685,19 @@ def csa_evict(weight: torch.Tensor, budget: int, idx_out: torch.Tensor,
     int32, the kept entries in ascending order, then -1; n_kept [B] int32."""
     if weight.dim() != 2:
         raise ValueError("weight must be [B, N_cap]")
+    B, dev = weight.shape[0], _same_device(weight)
+    _evict(weight, budget, _shape(idx_out, (B, budget), "idx_out", dev, torch.int32),
+           _shape(n_kept, (B,), "n_kept", dev, torch.int32), recent, n_entries, stream)
+
+
+def _evict(weight, budget, idx_out, n_kept, recent, n_entries, stream):
+    if weight.dim() != 2:
+        raise ValueError("weight must be [B, N_cap]")
     B, N_cap = weight.shape
     dev = _same_device(weight)
     _check(load().csa_evict(_shape(weight, (B, N_cap), "weight", dev, torch.float32), B, N_cap,
                             _shape(n_entries, (B,), "n_entries", dev, torch.int32), budget, recent,
-                            _shape(idx_out, (B, budget), "idx_out", dev, torch.int32),
-                            _shape(n_kept, (B,), "n_kept", dev, torch.int32), _stream(stream)))
+                            idx_out, n_kept, _stream(stream)))
 
 
 # ---------------------------------------------------------------- allocating wrappers
@@ -729,36 +760,49 @@ def hca_attn(q, kv_c, m: int, kv_raw, window: int, with_lse: bool = False, **kw)
     return (out, lse) if with_lse else out
 
 
-def rope(x, freqs, pos=None, y=None, **kw):
+# (these hand the outputs that they have just allocated on unchecked: the smallest calls'
+# kernels take a few us, less than the checks, allocations and the launch together)
+def rope(x, freqs, pos=None, y=None, rot_offset: int = 0, interleaved: bool = True, scale: float = 1.0,
+         pos0: int = 0, pos_step: int = 1, transpose: bool = False, stream=None):
     """Allocating form of csa_rope: (x rotated, y rotated or None)."""
     out = torch.empty_like(x, memory_format=torch.contiguous_format)
     y_out = None if y is None else torch.empty_like(y, memory_format=torch.contiguous_format)
-    csa_rope(x, out, freqs, y=y, y_out=y_out, pos=pos, **kw)
+    _rope(x, out, freqs, y, y_out, pos, rot_offset, interleaved, scale, pos0, pos_step, transpose,
+          stream, True)
     return out, y_out
 
 
-def hca_attn_prefix(q, kv_p, kv_c, m: int, kv_raw, window: int, with_lse: bool = False, **kw):
+def hca_attn_prefix(q, kv_p, kv_c, m: int, kv_raw, window: int, with_lse: bool = False, n_entries=None,
+                    raw_pos0=None, raw_len=None, q_pos=None, softmax_scale: float = 0.0,
+                    workspace=None, stream=None):
+    """Allocating form of hca_dense_attn_prefix: out, or (out, lse)."""
     out, lse = torch.empty_like(q), None
     if with_lse:
         B, n_q, H, _ = q.shape
         lse = torch.empty(B, n_q, H, dtype=torch.float32, device=q.device)
-    hca_dense_attn_prefix(q, kv_p, kv_c, m, kv_raw, window, out, lse_out=lse, **kw)
+    _prefix(q, kv_p, kv_c, m, kv_raw, window, None, None, n_entries, raw_pos0, raw_len, q_pos,
+            softmax_scale, workspace, stream, out, lse)
     return (out, lse) if with_lse else out
 
 
-def entry_weights(q, kv_c, m: int, lse, weight=None, **kw) -> torch.Tensor:
+def entry_weights(q, kv_c, m: int, lse, weight=None, idx=None, n_entries=None, q_pos=None,
+                  softmax_scale: float = 0.0, stream=None) -> torch.Tensor:
     """Allocating form of hca_entry_weights: weight (or 0) + what each entry received."""
-    B, N_cap, _ = kv_c.shape
-    out = torch.empty(B, N_cap, dtype=torch.float32, device=kv_c.device)
-    hca_entry_weights(q, kv_c, m, lse, out, weight_in=weight, **kw)
+    if weight is None:
+        B, N_cap, _ = kv_c.shape
+        out = torch.empty(B, N_cap, dtype=torch.float32, device=kv_c.device)
+    else:                                          # (its own shape and type are checked)
+        out = torch.empty_like(weight)
+    _weights(q, kv_c, m, lse, out.data_ptr(), weight, idx, n_entries, q_pos, softmax_scale, stream)
     return out
 
 
 def evict(weight, budget: int, recent: int = 0, n_entries=None, stream=None):
     """Allocating form of csa_evict: (idx, n_kept); weight is updated in place."""
-    idx = torch.empty(weight.shape[0], budget, dtype=torch.int32, device=weight.device)
-    n_kept = torch.empty(weight.shape[0], dtype=torch.int32, device=weight.device)
-    csa_evict(weight, budget, idx, n_kept, recent=recent, n_entries=n_entries, stream=stream)
+    B = weight.shape[0]
+    idx = torch.empty(B, budget, dtype=torch.int32, device=weight.device)
+    n_kept = torch.empty(B, dtype=torch.int32, device=weight.device)
+    _evict(weight, budget, idx.data_ptr(), n_kept.data_ptr(), recent, n_entries, stream)
     return idx, n_kept
 
 
