@@ -509,18 +509,23 @@ def rope_freqs(d_rot: int, base: float = 10000.0, factor: float = 1.0, original_
 _STRIDES = ctypes.c_longlong * 4
 
 
+def _token_strides(t: torch.Tensor, name: str):
+    """The token and head stride of t [B, n, H, D], whose elements are n tokens apart."""
+    B, n, H, D = t.shape
+    s0, s1, s2, s3 = t.stride()
+    if t.is_contiguous():
+        return H * D, D
+    if (D > 1 and s3 != 1) or (B > 1 and n > 0 and s0 != n * s1 and n != 1):
+        raise ValueError(f"{name}: channels must be contiguous and elements n tokens apart")
+    return (s0 if n == 1 and B > 1 else s1), s2
+
+
 def _rope_strides(x: torch.Tensor, out: torch.Tensor, name: str):
-    """{token, head} strides of x and of out, whose elements are n tokens apart."""
+    """{token, head} strides of x and of out."""
     B, n, H, D = x.shape
     st, spans = [], []
     for t in (x, out):
-        s0, s1, s2, s3 = t.stride()
-        if t.is_contiguous():
-            s1, s2 = H * D, D
-        elif (D > 1 and s3 != 1) or (B > 1 and n > 0 and s0 != n * s1 and n != 1):
-            raise ValueError(f"{name}: channels must be contiguous and elements n tokens apart")
-        elif n == 1 and B > 1:
-            s1 = s0
+        s1, s2 = _token_strides(t, name)
         st += [s1, s2]
         e = t.element_size()
         spans.append((t.data_ptr(), t.data_ptr() + ((B * n - 1) * s1 + (H - 1) * s2 + D) * e))
@@ -548,8 +553,9 @@ def _rope_tensor(x: torch.Tensor | None, out: torch.Tensor | None, B: int, n: in
         raise ValueError(f"the output of {name} must have its shape and dtype")
     if dev < 0 or x.get_device() != dev:
         _refuse_device(x, name, dev)
-    if fresh and x.is_contiguous():
-        return x.data_ptr(), out.data_ptr(), sh[2], None
+    if fresh:
+        st = None if x.is_contiguous() else _STRIDES(*_token_strides(x, name), sh[2] * D, D)
+        return x.data_ptr(), out.data_ptr(), sh[2], st
     if out.get_device() != dev:
         _refuse_device(out, name, dev)
     xp, op = x.data_ptr(), out.data_ptr()
