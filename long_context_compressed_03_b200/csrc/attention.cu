@@ -53,6 +53,7 @@ __global__ void __launch_bounds__(kThreads) attn_generic_kernel(AttnArgs a) {
 
     int C = 1, rank = 0;
     if constexpr (kSplit) {
+        grid_wait();
         C = (int)cg::this_cluster().num_blocks();
         rank = (int)cg::this_cluster().block_rank();
     }
@@ -219,13 +220,15 @@ cudaError_t launch_t(const AttnArgs& a, cudaStream_t s) {
         cfg.blockDim = dim3(kThreads);
         cfg.dynamicSmemBytes = smem;
         cfg.stream = s;
-        cudaLaunchAttribute attr[1];
+        cudaLaunchAttribute attr[2];
+        attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[1].val.programmaticStreamSerializationAllowed = 1;
         attr[0].id = cudaLaunchAttributeClusterDimension;
         attr[0].val.clusterDim.x = (unsigned)C;
         attr[0].val.clusterDim.y = 1;
         attr[0].val.clusterDim.z = 1;
         cfg.attrs = attr;
-        cfg.numAttrs = 1;
+        cfg.numAttrs = 2;
         e = cudaLaunchKernelEx(&cfg, kern, a);
         count_launch();
         return e != cudaSuccess ? e : cudaGetLastError();

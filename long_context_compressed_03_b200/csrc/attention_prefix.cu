@@ -303,6 +303,7 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     const int c = blockIdx.x, n_cta = gridDim.x;
     const int u0 = first_unit(p, c, n_cta), u1 = end_unit(p, c, n_cta);
 
+    grid_wait();
     if (threadIdx.x == 0) {
         // a CTA started after another one timed out does no work
         const bool dead = *reinterpret_cast<volatile uint32_t*>(p.err) != 0u;
@@ -795,7 +796,7 @@ prefix_join_kernel(const __grid_constant__ PrefixParams p, int n_cta) {
     const int r = threadIdx.x & (kRows - 1), grp = threadIdx.x / kRows;
     const long x = (long)u * n_cta, y = x + n_cta;
     const int c0 = (int)(x / p.U), n = (int)((y + p.U - 1) / p.U) - c0;      // the unit's parts
-    asm volatile("griddepcontrol.wait;" ::: "memory");                      // the parts are there
+    grid_wait();                                                            // the parts are there
     if (n <= 1) return;                                                     // written whole
     const long orow = (long)u * kRows + r;
     const float* ws = p.ws + (size_t)u * p.parts * kPartFloats;
@@ -974,9 +975,8 @@ cudaError_t launch_attention_prefix_tc(const AttnArgs& a, void* workspace, uint3
                           : (lse ? attn_prefix_kernel<1, true> : attn_prefix_kernel<1, false>);
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
     if (e != cudaSuccess) return e;
-    kern<<<(unsigned)pl.n_cta, kThreads, kSmem, s>>>(tm_q, tm_p, tm_c, tm_w, p);
+    e = launch_dependent(kern, (unsigned)pl.n_cta, kThreads, kSmem, s, tm_q, tm_p, tm_c, tm_w, p);
     count_launch();
-    e = cudaGetLastError();
     if (e != cudaSuccess || !cut) return e;
     // (A dependent launch whose start nothing triggers before the parts are written: it
     // only spares the gap between the two, 41.1 -> 39.9 us a call for 101 units issued one
@@ -984,17 +984,10 @@ cudaError_t launch_attention_prefix_tc(const AttnArgs& a, void* workspace, uint3
     // threads a row throughout, one CTA fills an SM, and 101 units of 2 to 3 parts took
     // 20 us.)
     const unsigned grid = (unsigned)(pl.U * (kD / kJoinCols));
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(grid);
-    cfg.stream = s;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    cfg.blockDim = dim3(pl.parts > 5 ? 4 * kRows : kRows);
-    if (pl.parts > 5) e = cudaLaunchKernelEx(&cfg, lse ? prefix_join_kernel<true, 4, 5> : prefix_join_kernel<false, 4, 5>, p, pl.n_cta);
-    else e = cudaLaunchKernelEx(&cfg, lse ? prefix_join_kernel<true, 1, 3> : prefix_join_kernel<false, 1, 3>, p, pl.n_cta);
+    const unsigned threads = pl.parts > 5 ? 4 * kRows : kRows;
+    const auto join = pl.parts > 5 ? (lse ? prefix_join_kernel<true, 4, 5> : prefix_join_kernel<false, 4, 5>)
+                                   : (lse ? prefix_join_kernel<true, 1, 3> : prefix_join_kernel<false, 1, 3>);
+    e = launch_dependent(join, grid, threads, 0, s, p, pl.n_cta);
     if (e != cudaSuccess) return e;
     count_launch();
     return cudaGetLastError();

@@ -8,6 +8,8 @@
 // listed entries receive weight.  Sums are fp32.
 #include <math.h>
 
+#include <algorithm>
+
 #include "common.cuh"
 #include "kernels.h"
 
@@ -19,12 +21,21 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kKeys = 32;
 constexpr float kLog2e = 1.4426950408889634f;
 
+// What the entries had (or zero), for the calls that add to listed entries only.
+__global__ void __launch_bounds__(kThreads) copy_weights_kernel(float* dst, const float* src, long n) {
+    grid_wait();
+    const long step = (long)gridDim.x * kThreads;
+#pragma unroll 4
+    for (long i = (long)blockIdx.x * kThreads + threadIdx.x; i < n; i += step) dst[i] = src ? src[i] : 0.0f;
+}
+
 // One CTA per 32 entries (or list slots): the keys staged as fp32, a lane per
 // key, the (query row, head) pairs dealt to the warps; the warps' sums are
 // added in warp order.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) weights_simt_kernel(WeightsArgs a) {
     extern __shared__ float sm[];
+    grid_wait();
     const int D = a.D, DP = D + 1;
     float* Ks = sm;                       // [32][D + 1]
     float* part = sm + kKeys * DP;        // [warps][32]
@@ -104,6 +115,7 @@ __global__ void __launch_bounds__(kMmaThreads) weights_mma_kernel(WeightsArgs a,
     __shared__ __align__(16) uint8_t Qs[2][kCols * RB];
     __shared__ float Ls[2][kCols];            // lse * log2(e); +inf: no weight
     __shared__ int Vs[2][kCols];              // entries the column's row sees
+    grid_wait();
     const int b = blockIdx.x / chunks, chunk = blockIdx.x - b * chunks;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, tq = lane & 3;
@@ -231,9 +243,9 @@ template <int D>
 cudaError_t launch_mma(const WeightsArgs& a, cudaStream_t s) {
     const int slots = a.idx ? a.topk : a.N_cap;
     const int chunks = (slots + kMmaKeys - 1) / kMmaKeys;
-    weights_mma_kernel<D><<<(unsigned)((long)chunks * a.B), kMmaThreads, 0, s>>>(a, chunks);
+    const cudaError_t e = launch_dependent(weights_mma_kernel<D>, (unsigned)((long)chunks * a.B), kMmaThreads, 0, s, a, chunks);
     count_launch();
-    return cudaGetLastError();
+    return e;
 }
 
 template <typename T>
@@ -241,18 +253,21 @@ cudaError_t launch_simt(const WeightsArgs& a, cudaStream_t s) {
     const int slots = a.idx ? a.topk : a.N_cap;
     const size_t smem = sizeof(float) * (kKeys * (a.D + 1) + kWarps * kKeys);
     const unsigned grid = (unsigned)((long)((slots + kKeys - 1) / kKeys) * a.B);
-    weights_simt_kernel<T><<<grid, kThreads, smem, s>>>(a);
+    const cudaError_t e = launch_dependent(weights_simt_kernel<T>, grid, kThreads, smem, s, a);
     count_launch();
-    return cudaGetLastError();
+    return e;
 }
 
 }  // namespace
 
 cudaError_t launch_entry_weights(const WeightsArgs& a, cudaStream_t s) {
     if (a.idx && a.out != a.in) {     // the unlisted entries keep what they had
-        const size_t bytes = sizeof(float) * (size_t)a.B * a.N_cap;
-        const cudaError_t e = a.in ? cudaMemcpyAsync(a.out, a.in, bytes, cudaMemcpyDeviceToDevice, s)
-                                   : cudaMemsetAsync(a.out, 0, bytes, s);
+        // (a kernel, and the next one set up meanwhile: 64 lists of 1999 of 8192 entries, calls
+        // one after the other, took 18.5 us with cudaMemcpyAsync)
+        const long n = (long)a.B * a.N_cap;
+        const unsigned grid = (unsigned)std::min<long>((n + 4 * kThreads - 1) / (4 * kThreads), 148L * 8);
+        const cudaError_t e = launch_dependent(copy_weights_kernel, grid, kThreads, 0, s, a.out, a.in, n);
+        count_launch();
         if (e != cudaSuccess) return e;
     }
     if ((a.idx ? a.topk : a.N_cap) == 0) return cudaSuccess;

@@ -191,6 +191,7 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         return __all_sync(0xffffffffu, try_wait(bar, parity));
     };
 
+    grid_wait();
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&ctl->full[i], 1);
@@ -584,9 +585,9 @@ cudaError_t launch_entry_weights_tc(const WeightsArgs& a, uint32_t* err, cudaStr
     const auto kern = p.steps == 1 ? weights_tc_kernel<true> : weights_tc_kernel<false>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
     if (e != cudaSuccess) return e;
-    kern<<<(unsigned)grid, kThreads, kSmem, s>>>(tm_k, tm_q, p);
+    e = launch_dependent(kern, (unsigned)grid, kThreads, kSmem, s, tm_k, tm_q, p);
     count_launch();
-    return cudaGetLastError();
+    return e;
 }
 
 }  // namespace csa

@@ -134,6 +134,7 @@ __global__ void __launch_bounds__(NT) evict_regs_kernel(EvictArgs a) {
     __shared__ int wgt[NW], weq[NW];
     const int b = blockIdx.x;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    grid_wait();
     float* w = a.weight + (size_t)b * a.N_cap;
     const int V = clampi(a.n_entries ? a.n_entries[b] : a.N_cap, 0, a.N_cap);
     int* idx = a.idx_out + (size_t)b * a.budget;
@@ -299,12 +300,13 @@ __global__ void __launch_bounds__(NT) evict_regs_kernel(EvictArgs a) {
 
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s) {
     // in registers where a CTA of 256 or 1024 threads holds the entries
-    if (a.N_cap <= 256 * 16) evict_regs_kernel<256, 16><<<(unsigned)a.B, 256, 0, s>>>(a);
-    else if (a.N_cap <= 1024 * 32) evict_regs_kernel<1024, 32><<<(unsigned)a.B, 1024, 0, s>>>(a);
+    cudaError_t e = cudaSuccess;
+    if (a.N_cap <= 256 * 16) e = launch_dependent(evict_regs_kernel<256, 16>, (unsigned)a.B, 256, 0, s, a);
+    else if (a.N_cap <= 1024 * 32) e = launch_dependent(evict_regs_kernel<1024, 32>, (unsigned)a.B, 1024, 0, s, a);
     else
         evict_kernel<<<(unsigned)a.B, kThreads, 0, s>>>(a);
     count_launch();
-    return cudaGetLastError();
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace csa

@@ -204,6 +204,7 @@ rope_vec_kernel(const __grid_constant__ RopeArgs a, const __grid_constant__ Rope
         slot = (slot + 1) % kDepth;
         asm volatile("cp.async.commit_group;" ::: "memory");             // (one a step, if empty)
     };
+    grid_wait();
 #pragma unroll
     for (int i = 0; i < kDepth - 1; ++i) load();
     fill_angles(a, tok0, n_tok, cs, ok);
@@ -289,9 +290,9 @@ cudaError_t launch_vec(const RopeArgs& a, cudaStream_t s) {
     auto kern = a.interleaved ? rope_vec_kernel<T, false> : rope_vec_kernel<T, true>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    kern<<<(unsigned)blocks, kThreads, smem, s>>>(a, g);
+    e = launch_dependent(kern, (unsigned)blocks, kThreads, smem, s, a, g);
     count_launch();
-    return cudaGetLastError();
+    return e;
 }
 
 // One pair or one passed-on element per thread and step: any size, stride and offset.
