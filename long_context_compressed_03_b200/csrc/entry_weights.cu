@@ -9,6 +9,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -16,10 +17,17 @@
 namespace csa {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr int kKeys = 32;
 constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float4 load4(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
+__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
+    const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+    return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u), __uint_as_float(v.y << 16),
+                       __uint_as_float(v.y & 0xffff0000u));
+}
 
 // What the entries had (or zero), for the calls that add to listed entries only.
 __global__ void __launch_bounds__(kThreads) copy_weights_kernel(float* dst, const float* src, long n) {
@@ -61,18 +69,39 @@ __global__ void __launch_bounds__(kThreads) weights_simt_kernel(WeightsArgs a) {
     const int s = ent[lane];
     const float sl2 = a.scale * kLog2e;
     float acc = 0.0f;
-    for (int r = warp; r < a.n_q * a.H; r += kWarps) {
-        const int qi = r / a.H;
-        const int t = a.q_pos ? a.q_pos[(size_t)b * a.n_q + qi] : qi;
-        const int vis = t < 0 ? 0 : (int)min(((unsigned)t + 1u) / (unsigned)a.m, (unsigned)ne);
-        const size_t row = (size_t)b * a.n_q * a.H + r;
-        const float lse = a.lse[row];
-        if (!(lse > -INFINITY) && lse == lse) continue;      // an empty row: no weight
-        const T* q = static_cast<const T*>(a.q) + row * D;
-        float z = 0.0f;
-        for (int d = 0; d < D; ++d) z = fmaf(to_f32(q[d]), Ks[lane * DP + d], z);
-        if (s >= 0 && s < vis) acc += exp2f(fmaf(z, sl2, -lse * kLog2e));
-    }
+    // Rows four at a time share the key's reads, the last few (or few rows) go one by one:
+    // 64 query rows of 8 heads over 4 x 1024 fp32 entries of 64 take 30 us; one by one on 8
+    // warps 128, by fours on 8 and 16 warps 64 and 37.
+    const int n = a.n_q * a.H, fours = n / (4 * kWarps) * (4 * kWarps);
+    const T* q0 = static_cast<const T*>(a.q) + (size_t)b * n * D;
+    const float* k = Ks + lane * DP;
+    const auto rows = [&](int r, auto count) {               // weights of rows r, r + 1, ..
+        constexpr int kCount = decltype(count)::value;
+        const T* q = q0 + (size_t)r * D;
+        float z[kCount];
+#pragma unroll
+        for (int j = 0; j < kCount; ++j) z[j] = 0.0f;
+#pragma unroll 4
+        for (int d = 0; d < D; d += 4) {
+            const float k0 = k[d], k1 = k[d + 1], k2 = k[d + 2], k3 = k[d + 3];
+#pragma unroll
+            for (int j = 0; j < kCount; ++j) {
+                const float4 x = load4(q + j * D + d);
+                z[j] = fmaf(x.w, k3, fmaf(x.z, k2, fmaf(x.y, k1, fmaf(x.x, k0, z[j]))));
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kCount; ++j) {
+            const int qi = (r + j) / a.H;
+            const int t = a.q_pos ? a.q_pos[(size_t)b * a.n_q + qi] : qi;
+            const int vis = t < 0 ? 0 : (int)min(((unsigned)t + 1u) / (unsigned)a.m, (unsigned)ne);
+            const float lse = a.lse[(size_t)b * n + r + j];
+            if (!(lse > -INFINITY) && lse == lse) continue;  // an empty row: no weight
+            if (s >= 0 && s < vis) acc += exp2f(fmaf(z[j], sl2, -lse * kLog2e));
+        }
+    };
+    for (int r = warp * 4; r < fours; r += kWarps * 4) rows(r, std::integral_constant<int, 4>{});
+    for (int r = fours + warp; r < n; r += kWarps) rows(r, std::integral_constant<int, 1>{});
     part[warp * kKeys + lane] = acc;
     __syncthreads();
     if (warp == 0 && s >= 0) {
