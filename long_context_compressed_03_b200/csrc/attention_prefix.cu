@@ -569,7 +569,7 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         // ------------------------------------------------------------ softmax and output
         // Group gr takes every other tile, thread h of a row 32 columns of each
         // 64-key half (id: which of the row's four threads).  P V of a half
-        // starts when its P is there, which frees the buffer sooner: 1490 -> RESULT
+        // starts when its P is there, which frees the buffer sooner: 1490 -> 1420
         // cycles a tile.
         const int gr = (warp - kSoftWarp0) >> 3, h = ((warp - kSoftWarp0) >> 2) & 1, id = 2 * gr + h;
         const int r = (warp & 3) * 32 + lane;                // row of the unit

@@ -70,6 +70,91 @@ __device__ __forceinline__ uint4 pack(const float* f, __nv_bfloat16) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// How a call is cut: tokens a CTA; rows a CTA of one token, and such CTAs a token; items
+// a row; rows a step of the CTA's threads.  The divisors come with their reciprocals
+// (the calls of a few us wait for every division).
+struct RopeGrid {
+    int tpb, rpb, chunks, ipr, row_step;
+    float inv_rot, inv_pass, inv_h[2], inv_step;
+};
+// x / d for 0 <= x < 2^20, given 1 / d
+__device__ __forceinline__ int quot(int x, float inv) { return (int)(((float)x + 0.5f) * inv); }
+
+// A CTA's rows: the hx x heads of its tokens, then their hy y heads.
+struct RopeTile {
+    long tok0;
+    int r0, n_tok, hx, hy, nx, rows, tpb, row_step;
+    float inv_x, inv_y;          // 1 / heads
+    __device__ __forceinline__ RopeTile(const RopeArgs& a, const RopeGrid& g) {
+        const long total = (long)a.B * a.n;
+        const int tile = g.chunks == 1 ? (int)blockIdx.x : (int)(blockIdx.x / g.chunks);
+        tpb = g.tpb;
+        row_step = g.row_step;
+        inv_x = g.inv_h[0];
+        inv_y = g.inv_h[1];
+        tok0 = (long)tile * tpb;
+        r0 = ((int)blockIdx.x - tile * g.chunks) * g.rpb;
+        n_tok = (int)min((long)tpb, total - tok0);
+        const int R = min(a.H[0] + a.H[1] - r0, g.rpb);
+        hx = min(max(a.H[0] - r0, 0), R);
+        hy = R - hx;
+        nx = n_tok * hx;
+        rows = n_tok * R;
+    }
+};
+// Walks the rows of one thread, row_step apart.
+template <typename T>
+struct Rows {
+    const T* p;
+    long inc, wrap;              // to the next row; and, past a token's last row, back to the next token's
+    int v, r, t, h, dr, dt;      // row, its head and token; heads a token; steps of r and t
+    __device__ __forceinline__ void row(const RopeTile& c, int at) {
+        const bool y = at >= c.nx;
+        v = at;
+        if (y) at -= c.nx;
+        if (c.tpb == 1) {        // (one token: no row is past its last)
+            h = 1 << 30;
+            t = dt = 0;
+            r = at;
+            dr = c.row_step;
+            return;
+        }
+        const float inv = y ? c.inv_y : c.inv_x;
+        h = y ? c.hy : c.hx;
+        t = quot(at, inv);
+        r = at - t * h;
+        dt = quot(c.row_step, inv);
+        dr = c.row_step - dt * h;
+    }
+    __device__ __forceinline__ void aim(const RopeArgs& a, const RopeTile& c, const void* const* ptr,
+                                        const long (*sd)[2], int e0) {
+        const bool y = v >= c.nx;
+        const long s0 = sd[y][0], s1 = sd[y][1];
+        inc = dt * s0 + dr * s1;
+        wrap = s0 - h * s1;
+        const int h0 = y ? max(c.r0 - a.H[0], 0) : c.r0;
+        p = static_cast<const T*>(ptr[y]) + (c.tok0 + t) * s0 + (h0 + r) * s1 + e0;
+    }
+    __device__ __forceinline__ void step(const RopeArgs& a, const RopeTile& c, const void* const* ptr,
+                                         const long (*sd)[2], int e0) {
+        const bool x = v < c.nx;
+        v += c.row_step;
+        if (x && v >= c.nx) {    // from the x heads to the y heads
+            row(c, v);
+            aim(a, c, ptr, sd, e0);
+            return;
+        }
+        t += dt;
+        r += dr;
+        p += inc;
+        if (r >= h) {
+            r -= h;
+            ++t;
+            p += wrap;
+        }
+    }
+};
+
 // 16 bytes a step: a CTA takes tpb tokens and all their rows (the heads of both
 // tensors, which share the angles), or rpb rows of one token.  A thread keeps one
 // item of a row -- a vector (interleaved: its pairs are inside; not rotated: passed
@@ -89,16 +174,6 @@ __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
                  ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
 }
 
-// How a call is cut: tokens a CTA; rows a CTA of one token, and such CTAs a token; items
-// a row; rows a step of the CTA's threads.  The divisors come with their reciprocals
-// (the calls of a few us wait for every division).
-struct RopeGrid {
-    int tpb, rpb, chunks, ipr, row_step;
-    float inv_rot, inv_pass, inv_h[2], inv_step;
-};
-// x / d for 0 <= x < 2^20, given 1 / d
-__device__ __forceinline__ int quot(int x, float inv) { return (int)(((float)x + 0.5f) * inv); }
-
 template <typename T, bool HALF>
 __global__ void __launch_bounds__(kThreads, 4)
 rope_vec_kernel(const __grid_constant__ RopeArgs a, const __grid_constant__ RopeGrid g) {
@@ -106,14 +181,9 @@ rope_vec_kernel(const __grid_constant__ RopeArgs a, const __grid_constant__ Rope
     extern __shared__ __align__(16) uint8_t smem[];
     float2* cs = reinterpret_cast<float2*>(smem + ring_bytes<HALF>());
     const int half = a.d_rot / 2;
-    const int tpb = g.tpb, ipr = g.ipr, row_step = g.row_step;
-    int* ok = reinterpret_cast<int*>(cs + (size_t)tpb * half);
-    const long total = (long)a.B * a.n;
-    const int tile = g.chunks == 1 ? (int)blockIdx.x : (int)(blockIdx.x / g.chunks);
-    const long tok0 = (long)tile * tpb;
-    const int r0 = ((int)blockIdx.x - tile * g.chunks) * g.rpb;
-    const int n_tok = (int)min((long)tpb, total - tok0);
-    const int R = min(a.H[0] + a.H[1] - r0, g.rpb);
+    const RopeTile c(a, g);
+    const int ipr = g.ipr, row_step = g.row_step;
+    int* ok = reinterpret_cast<int*>(cs + (size_t)g.tpb * half);
     const int rot_items = (HALF ? half : a.d_rot) / V, pass_items = ipr - rot_items;
     // Rotated items to the first threads, the others to the rest: a warp of both kinds
     // would run the rotation for a third of its lanes.  (So mapped, and with every row's
@@ -134,71 +204,20 @@ rope_vec_kernel(const __grid_constant__ RopeArgs a, const __grid_constant__ Rope
     if (rot) e0 += a.off;
     else if (e0 >= a.off) e0 += a.d_rot;
     const int pair0 = HALF ? it * V : it * (V / 2);
-    // The CTA's rows: the hx x heads of its tokens, then their hy y heads.  A thread's
-    // rows are row_step apart.
-    const int hx = min(max(a.H[0] - r0, 0), R), hy = R - hx;
-    const int nx = n_tok * hx, rows = n_tok * R;
-    struct Rows {                // walks them
-        const T* p;
-        long inc, wrap;          // to the next row; and, past a token's last row, back to the next token's
-        int v, r, t, h, dr, dt;  // row, its head and token; heads a token; steps of r and t
-    };
-    const auto row = [&](Rows& w, int v) {
-        const bool y = v >= nx;
-        w.v = v;
-        if (y) v -= nx;
-        if (tpb == 1) {          // (one token: no row is past its last)
-            w.h = 1 << 30;
-            w.t = w.dt = 0;
-            w.r = v;
-            w.dr = row_step;
-            return;
-        }
-        w.h = y ? hy : hx;
-        w.t = quot(v, g.inv_h[y]);
-        w.r = v - w.t * w.h;
-        w.dt = quot(row_step, g.inv_h[y]);
-        w.dr = row_step - w.dt * w.h;
-    };
-    const auto aim = [&](Rows& w, const void* const* ptr, const long(*sd)[2]) {
-        const bool y = w.v >= nx;
-        const long s0 = sd[y][0], s1 = sd[y][1];
-        w.inc = w.dt * s0 + w.dr * s1;
-        w.wrap = s0 - w.h * s1;
-        const int h0 = y ? max(r0 - a.H[0], 0) : r0;
-        w.p = static_cast<const T*>(ptr[y]) + (tok0 + w.t) * s0 + (h0 + w.r) * s1 + e0;
-    };
-    const auto step = [&](Rows& w, const void* const* ptr, const long(*sd)[2]) {
-        const bool x = w.v < nx;
-        w.v += row_step;
-        if (x && w.v >= nx) {    // from the x heads to the y heads
-            row(w, w.v);
-            aim(w, ptr, sd);
-            return;
-        }
-        w.t += w.dt;
-        w.r += w.dr;
-        w.p += w.inc;
-        if (w.r >= w.h) {
-            w.r -= w.h;
-            ++w.t;
-            w.p += w.wrap;
-        }
-    };
-    Rows in, out;
-    row(in, rr0);
+    Rows<T> in, out;
+    in.row(c, rr0);
     out = in;
-    aim(in, a.x, a.xs);
+    in.aim(a, c, a.x, a.xs, e0);
     uint4* ring = reinterpret_cast<uint4*>(smem) + threadIdx.x;          // [kDepth][1 or 2][kThreads]
     constexpr int kSlot = (HALF ? 2 : 1) * kThreads;
-    int left = rr0 < row_step && rows > rr0 ? quot(rows - rr0 + row_step - 1, g.inv_step) : 0;
+    int left = rr0 < row_step && c.rows > rr0 ? quot(c.rows - rr0 + row_step - 1, g.inv_step) : 0;
     int count = left, slot = 0;
     const auto load = [&]() {
         if (left > 0) {
             uint4* d = ring + slot * kSlot;
             cp_async16(d, in.p);
             if (HALF && rot) cp_async16(d + kThreads, in.p + half);
-            step(in, a.x, a.xs);
+            in.step(a, c, a.x, a.xs, e0);
             --left;
         }
         slot = (slot + 1) % kDepth;
@@ -207,8 +226,8 @@ rope_vec_kernel(const __grid_constant__ RopeArgs a, const __grid_constant__ Rope
     grid_wait();
 #pragma unroll
     for (int i = 0; i < kDepth - 1; ++i) load();
-    fill_angles(a, tok0, n_tok, cs, ok);
-    aim(out, a.out, a.os);
+    fill_angles(a, c.tok0, c.n_tok, cs, ok);
+    out.aim(a, c, a.out, a.os, e0);
     for (; count > 0; --count) {
         asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 2) : "memory");
         const uint4* d = ring + (slot + 1) % kDepth * kSlot;
@@ -218,14 +237,14 @@ rope_vec_kernel(const __grid_constant__ RopeArgs a, const __grid_constant__ Rope
         const int st = out.t;
         T* p = const_cast<T*>(out.p);
         if (rot && ok[st]) {
-            const float2* c = cs + st * half + pair0;
+            const float2* angle = cs + st * half + pair0;
             float x[V], y[V];
             unpack(v, x, T());
             if (HALF) {
                 unpack(w, y, T());
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    const float2 q = c[i];
+                    const float2 q = angle[i];
                     const float p0 = x[i] * q.x - y[i] * q.y, p1 = y[i] * q.x + x[i] * q.y;
                     x[i] = p0;
                     y[i] = p1;
@@ -234,7 +253,7 @@ rope_vec_kernel(const __grid_constant__ RopeArgs a, const __grid_constant__ Rope
             } else {
 #pragma unroll
                 for (int i = 0; i < V / 2; ++i) {
-                    const float2 q = c[i];
+                    const float2 q = angle[i];
                     const float p0 = x[2 * i] * q.x - x[2 * i + 1] * q.y, p1 = x[2 * i + 1] * q.x + x[2 * i] * q.y;
                     x[2 * i] = p0;
                     x[2 * i + 1] = p1;
@@ -244,7 +263,7 @@ rope_vec_kernel(const __grid_constant__ RopeArgs a, const __grid_constant__ Rope
         }
         *reinterpret_cast<uint4*>(p) = v;
         if (HALF && rot) *reinterpret_cast<uint4*>(p + half) = w;
-        step(out, a.out, a.os);
+        out.step(a, c, a.out, a.os, e0);
     }
 }
 
@@ -258,35 +277,49 @@ bool vec_supported(const RopeArgs& a) {
     return true;
 }
 
-template <typename T>
-cudaError_t launch_vec(const RopeArgs& a, cudaStream_t s) {
-    constexpr int V = 16 / sizeof(T);
+// Cuts a call whose rows have rot_items and pass_items.
+RopeGrid cut(const RopeArgs& a, int rot_items, int pass_items, long* blocks) {
     const long total = (long)a.B * a.n;
-    // in place, the channels that are not rotated are already there
-    const bool in_place = (!a.H[0] || a.x[0] == a.out[0]) && (!a.H[1] || a.x[1] == a.out[1]);
-    const int R = a.H[0] + a.H[1];
-    const int ipr = (a.interleaved ? a.d_rot : a.d_rot / 2) / V + (in_place ? 0 : (a.D - a.d_rot) / V);
+    const int R = a.H[0] + a.H[1], ipr = rot_items + pass_items;
     // Rows a CTA: kDepth a thread, fewer where the call has too few rows for
     // the GPU (148 SMs, two CTAs each); whole tokens where a token's rows fit.  With
     // rows for 16 CTAs an SM, up to 8 times that: making one token's angles a CTA, by one
     // warp, cost more than moving its rows.
-    const int step = kThreads / ipr, pass = step * kDepth;
+    const int step = std::max(kThreads / ipr, 1), pass = step * kDepth;
     const int want = (int)std::max<long>(std::min<long>(std::max<long>(total * R / (2 * 148), step), pass),
                                          std::min<long>(total * R / (16 * 148), 8L * pass));
-    int tpb = 1, rpb = R, chunks = 1;
+    RopeGrid g{1, R, 1, ipr, step, 0.0f, 0.0f, {0.0f, 0.0f}, 0.0f};
     if (want >= R) {
-        tpb = std::max(1, std::min(want / R, 4096 / (a.d_rot / 2)));      // angles: 32 KB at most
+        g.tpb = std::max(1, std::min(want / R, 4096 / (a.d_rot / 2)));    // angles: 32 KB at most
     } else {
-        chunks = (R + want - 1) / want;
-        rpb = (R + chunks - 1) / chunks;
+        g.chunks = (R + want - 1) / want;
+        g.rpb = (R + g.chunks - 1) / g.chunks;
     }
     const auto inv = [](int d) { return d > 0 ? 1.0f / (float)d : 0.0f; };
-    const int rot_items = (a.interleaved ? a.d_rot : a.d_rot / 2) / V;
-    const RopeGrid g{tpb, rpb, chunks, ipr, step, inv(rot_items), inv(ipr - rot_items), {inv(a.H[0]), inv(a.H[1])}, inv(step)};
-    const long blocks = (total + tpb - 1) / tpb * chunks;
+    g.inv_rot = inv(rot_items);
+    g.inv_pass = inv(pass_items);
+    g.inv_h[0] = inv(a.H[0]);
+    g.inv_h[1] = inv(a.H[1]);
+    g.inv_step = inv(step);
+    *blocks = (total + g.tpb - 1) / g.tpb * g.chunks;
+    return g;
+}
+size_t angle_bytes(const RopeArgs& a, const RopeGrid& g) {
+    return (size_t)g.tpb * (a.d_rot / 2) * sizeof(float2) + g.tpb * sizeof(int);
+}
+// In place, the channels that are not rotated are already there.
+int pass_channels(const RopeArgs& a) {
+    const bool in_place = (!a.H[0] || a.x[0] == a.out[0]) && (!a.H[1] || a.x[1] == a.out[1]);
+    return in_place ? 0 : a.D - a.d_rot;
+}
+
+template <typename T>
+cudaError_t launch_vec(const RopeArgs& a, cudaStream_t s) {
+    constexpr int V = 16 / sizeof(T);
+    long blocks;
+    const RopeGrid g = cut(a, (a.interleaved ? a.d_rot : a.d_rot / 2) / V, pass_channels(a) / V, &blocks);
     if (blocks > (1L << 31) - 1) return cudaErrorInvalidConfiguration;
-    const size_t smem = (a.interleaved ? ring_bytes<false>() : ring_bytes<true>()) +
-                        (size_t)tpb * (a.d_rot / 2) * sizeof(float2) + tpb * sizeof(int);
+    const size_t smem = (a.interleaved ? ring_bytes<false>() : ring_bytes<true>()) + angle_bytes(a, g);
     auto kern = a.interleaved ? rope_vec_kernel<T, false> : rope_vec_kernel<T, true>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
@@ -295,63 +328,82 @@ cudaError_t launch_vec(const RopeArgs& a, cudaStream_t s) {
     return e;
 }
 
-// One pair or one passed-on element per thread and step: any size, stride and offset.
+// The same for any size, stride and offset: a thread keeps one pair, or one element
+// that is passed on, and goes down the rows, kBatch of them in flight.  (With an item's
+// row, head and token divided out for each: 46 us for 2 x 4096 tokens of 17 x 80 bf16, 50
+// rotated.)
+constexpr int kBatch = 4;
+
 template <typename T>
-__global__ void __launch_bounds__(kThreads) rope_scalar_kernel(RopeArgs a, int tpb) {
-    extern __shared__ float2 cs[];
+__global__ void __launch_bounds__(kThreads) rope_item_kernel(const __grid_constant__ RopeArgs a,
+                                                             const __grid_constant__ RopeGrid g) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    float2* cs = reinterpret_cast<float2*>(smem);
     const int half = a.d_rot / 2;
-    int* ok = reinterpret_cast<int*>(cs + (size_t)tpb * half);
-    const long total = (long)a.B * a.n;
-    const long tok0 = (long)blockIdx.x * tpb;
-    const int n_tok = (int)min((long)tpb, total - tok0);
-    fill_angles(a, tok0, n_tok, cs, ok);
-    const int R = a.H[0] + a.H[1];
-    const int ipr = half + (a.D - a.d_rot);
-    for (int i = threadIdx.x; i < n_tok * R * ipr; i += blockDim.x) {
-        const int rr = i / ipr, it = i - rr * ipr;
-        const int t = rr / R, r = rr - t * R;
-        const int w = r >= a.H[0];
-        const int h = w ? r - a.H[0] : r;
-        const T* src = static_cast<const T*>(a.x[w]) + (tok0 + t) * a.xs[w][0] + h * a.xs[w][1];
-        T* dst = static_cast<T*>(a.out[w]) + (tok0 + t) * a.os[w][0] + h * a.os[w][1];
-        if (it < half) {
-            const int ea = a.off + (a.interleaved ? 2 * it : it);
-            const int eb = ea + (a.interleaved ? 1 : half);
-            if (!ok[t]) {
-                const T u = src[ea], v = src[eb];
-                dst[ea] = u;
-                dst[eb] = v;
-                continue;
+    int* ok = reinterpret_cast<int*>(cs + (size_t)g.tpb * half);
+    const RopeTile c(a, g);
+    grid_wait();
+    fill_angles(a, c.tok0, c.n_tok, cs, ok);
+    // (rows of more items than threads: one row a step, its items in turn)
+    const int rr0 = g.ipr <= kThreads ? (int)threadIdx.x / g.ipr : 0;
+    if (rr0 >= c.row_step) return;
+    for (int it = (int)threadIdx.x - rr0 * g.ipr; it < g.ipr; it += kThreads) {
+        const bool rot = it < half;
+        int e0 = a.off + (a.interleaved ? 2 * it : it);
+        if (!rot) {
+            e0 = it - half;
+            if (e0 >= a.off) e0 += a.d_rot;
+        }
+        const int e1 = a.interleaved ? 1 : half;             // from a pair's first element to its second
+        Rows<T> in, out;
+        in.row(c, rr0);
+        out = in;
+        in.aim(a, c, a.x, a.xs, e0);
+        out.aim(a, c, a.out, a.os, e0);
+        while (out.v < c.rows) {
+            T u[kBatch], w[kBatch];
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b) {
+                if (in.v >= c.rows) continue;
+                u[b] = in.p[0];
+                if (rot) w[b] = in.p[e1];
+                in.step(a, c, a.x, a.xs, e0);
             }
-            const float u = to_f32(src[ea]), v = to_f32(src[eb]);
-            const float2 c = cs[t * half + it];
-            store_out<T>(dst + ea, u * c.x - v * c.y);
-            store_out<T>(dst + eb, v * c.x + u * c.y);
-        } else {
-            int e = it - half;
-            if (e >= a.off) e += a.d_rot;
-            dst[e] = src[e];
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b) {
+                if (out.v >= c.rows) continue;
+                T* p = const_cast<T*>(out.p);
+                if (rot && ok[out.t]) {
+                    const float x = to_f32(u[b]), y = to_f32(w[b]);
+                    const float2 q = cs[out.t * half + it];
+                    store_out<T>(p, x * q.x - y * q.y);
+                    store_out<T>(p + e1, y * q.x + x * q.y);
+                } else {
+                    p[0] = u[b];
+                    if (rot) p[e1] = w[b];
+                }
+                out.step(a, c, a.out, a.os, e0);
+            }
         }
     }
 }
 
 template <typename T>
-cudaError_t launch_scalar(const RopeArgs& a, cudaStream_t s) {
-    const long total = (long)a.B * a.n;
-    const int items = (a.H[0] + a.H[1]) * (a.d_rot / 2 + a.D - a.d_rot);
-    const int tpb = items >= 1024 ? 1 : (items >= 256 ? 4 : 16);
-    const size_t smem = (size_t)tpb * (a.d_rot / 2) * sizeof(float2) + tpb * sizeof(int);
-    rope_scalar_kernel<T><<<(unsigned)((total + tpb - 1) / tpb), kThreads, smem, s>>>(a, tpb);
+cudaError_t launch_items(const RopeArgs& a, cudaStream_t s) {
+    long blocks;
+    const RopeGrid g = cut(a, a.d_rot / 2, pass_channels(a), &blocks);
+    if (blocks > (1L << 31) - 1) return cudaErrorInvalidConfiguration;
+    const cudaError_t e = launch_dependent(rope_item_kernel<T>, (unsigned)blocks, kThreads, angle_bytes(a, g), s, a, g);
     count_launch();
-    return cudaGetLastError();
+    return e;
 }
 
 }  // namespace
 
 cudaError_t launch_rope(const RopeArgs& a, cudaStream_t s) {
     // 16-byte items need sizes and strides that are whole vectors
-    if (a.dt == DT_F32) return vec_supported<float>(a) ? launch_vec<float>(a, s) : launch_scalar<float>(a, s);
-    return vec_supported<__nv_bfloat16>(a) ? launch_vec<__nv_bfloat16>(a, s) : launch_scalar<__nv_bfloat16>(a, s);
+    if (a.dt == DT_F32) return vec_supported<float>(a) ? launch_vec<float>(a, s) : launch_items<float>(a, s);
+    return vec_supported<__nv_bfloat16>(a) ? launch_vec<__nv_bfloat16>(a, s) : launch_items<__nv_bfloat16>(a, s);
 }
 
 }  // namespace csa
