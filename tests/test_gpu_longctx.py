@@ -63,6 +63,27 @@ def test_rope(dt, interleaved, B, n, H, Hy, D, rot, off):
         assert torch.equal(xi, out[0]) and (y is None or torch.equal(yi, out[1]))
 
 
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("interleaved", [True, False])
+@pytest.mark.parametrize("B,n,H,Hy,D,rot,off", [
+    # rotated parts that are no whole vectors, in rows that are and are not; many tokens a CTA,
+    # one token's rows over several CTAs, rows of more items than a CTA's threads
+    (2, 700, 17, 1, 80, 50, 0), (1, 3, 300, 2, 192, 50, 142), (3, 1, 64, 1, 80, 50, 30), (1, 260, 2, 2, 36, 6, 5),
+    (1, 4, 3, 1, 1100, 250, 3), (1, 4, 2, 0, 1104, 256, 8), (4, 90, 1, 1, 16, 2, 7), (64, 2, 3, 2, 64, 64, 0)])
+def test_rope_of_odd_parts_and_in_place(dt, interleaved, B, n, H, Hy, D, rot, off):
+    g = gen(B * 1000 + n + D)
+    x, y = normal(g, dt, B, n, H, D), normal(g, dt, B, n, Hy, D) if Hy else None
+    pos = torch.randint(-1, 1 << 20, (B, n), generator=g, device=DEV, dtype=torch.int32)
+    freqs, _ = api.rope_freqs(rot)
+    out = api.rope(x, freqs, pos=pos, y=y, rot_offset=off, interleaved=interleaved)
+    for t, o in zip((x, y), out):
+        if t is not None:
+            want, bound = ref.rope(t, pos, freqs, off, interleaved, 1.0, False)
+            within(o, want, bound, "rope")
+    api.csa_rope(x, x, freqs, y=y, y_out=y, pos=pos, rot_offset=off, interleaved=interleaved)
+    assert torch.equal(x, out[0]) and (y is None or torch.equal(y, out[1]))
+
+
 @pytest.mark.parametrize("dt,D,extra", [(BF, 128, 1), (F32, 64, 3), (BF, 24, 1)])
 def test_rope_strided_views_and_default_positions(dt, D, extra):
     g, B, n, H = gen(3), 2, 17, 6
