@@ -82,7 +82,8 @@ cudaError_t launch_dependent(void (*kern)(P...), unsigned grid, unsigned block, 
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, std::forward<A>(args)...);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, std::forward<A>(args)...);
+    return e == cudaSuccess ? e : cudaGetLastError();        // (reported once, not to a later launch too)
 }
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
