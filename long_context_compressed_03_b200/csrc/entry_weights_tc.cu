@@ -6,7 +6,8 @@
 // one key over its columns in registers: no cross-lane sums, no atomics, and a
 // key that no row sees can hold anything, since it touches its own lane only.
 // Work item: 128 entries (or list slots) of one element, all columns in steps of
-// 128.  Persistent, one CTA per SM; item i is tile i / B of element i mod B, so the
+// 128 (where a cluster shares an item, a run of the steps a CTA).  Persistent, one CTA
+// per SM; item i is tile i / B of element i mod B, so the
 // tiles past the elements' ends come last and cost nothing.
 // Roles (24 warps): warp 0 loads Q and the entries' tiles (TMA); warps 1-2 stage
 // the columns' lse and reach; warps 3-6 gather listed entries row by row
@@ -23,6 +24,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -47,6 +49,7 @@ constexpr int kThreads = (kSumWarp0 + kSumWarps) * 32;
 constexpr int kNe = 1024;                   // elements whose entry count is kept in shared memory
 constexpr int kSms = 148;
 constexpr int kXs = 8;                      // items whose other quarters' sums may wait
+constexpr int kCx = 24, kRounds = 8;         // a cluster's sums that may wait; its items, at most
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct __align__(16) Ctrl {
@@ -58,17 +61,19 @@ struct __align__(16) Ctrl {
     uint64_t full[kStages], freeb[kStages];        // Q
     uint64_t kfull[kKBufs], kfree[kKBufs];
     uint64_t s_full[kBufs], s_free[kBufs];         // scores, and the columns' lse and reach
-    uint64_t x_full[kXs];
+    float cx[kCx][kKeys];                   // the other CTAs' sums (in the cluster's first)
+    uint64_t x_full[kXs], c_full[kRounds];
     uint64_t fin, stall_bar;     // (stall_bar: a barrier that nothing completes, for tests)
     uint32_t tmem_base;
     int abort;
+    int cshift;                  // log2 of the CTAs that share an item in this call
 };
 constexpr size_t kSmem = 1024 + (kKBufs + kStages) * kTileBytes + sizeof(Ctrl);
 
 struct TcWeights {
     WeightsArgs a;
     int items, steps, cols;
-    int dchunk, db;              // a grid's width in (tiles, elements)
+    int cshift;                  // log2 of a cluster's CTAs
     int hshift, mshift;          // log2 of H and m where they are powers of two, else -1
     int qbox;                    // Q rows a TMA copy brings: 64 where no step has more columns, else 128
     float sl2;
@@ -142,7 +147,18 @@ __device__ __forceinline__ float sum_columns(uint32_t taddr, const float* nlse, 
 __device__ __forceinline__ int entries_of(const WeightsArgs& a, int b) {
     return clampi(a.n_entries ? __ldg(a.n_entries + b) : a.N_cap, 0, a.N_cap);
 }
-// A CTA's items, one grid's width apart: tile i / B of element i mod B.
+// A CTA's items, `width` apart (dchunk tiles and db elements): tile i / B of element i mod B.
+struct Walk {
+    int first, width, dchunk, db;
+};
+__device__ __forceinline__ Walk walk_of(const TcWeights& p, int shared) {
+    Walk w;
+    w.first = (int)blockIdx.x >> shared;
+    w.width = (int)gridDim.x >> shared;
+    w.dchunk = w.width / p.a.B;
+    w.db = w.width - w.dchunk * p.a.B;
+    return w;
+}
 struct Item {
     int i, b, chunk, ne;
     bool live;               // some key of it can be seen
@@ -152,18 +168,18 @@ __device__ __forceinline__ void look(const TcWeights& p, const int* ne, Item& t)
     if (t.i < p.items) t.ne = t.b < kNe ? ne[t.b] : entries_of(p.a, t.b);
     t.live = p.a.idx ? t.ne > 0 : t.chunk * kKeys < t.ne;
 }
-__device__ __forceinline__ Item first_item(const TcWeights& p, const int* ne) {
+__device__ __forceinline__ Item first_item(const TcWeights& p, const Walk& w, const int* ne) {
     Item t;
-    t.i = blockIdx.x;
+    t.i = w.first;
     t.chunk = t.i / p.a.B;
     t.b = t.i - t.chunk * p.a.B;
     look(p, ne, t);
     return t;
 }
-__device__ __forceinline__ void next_item(const TcWeights& p, const int* ne, Item& t) {
-    t.i += gridDim.x;
-    t.chunk += p.dchunk;
-    t.b += p.db;
+__device__ __forceinline__ void next_item(const TcWeights& p, const Walk& w, const int* ne, Item& t) {
+    t.i += w.width;
+    t.chunk += w.dchunk;
+    t.b += w.db;
     if (t.b >= p.a.B) {
         t.b -= p.a.B;
         ++t.chunk;
@@ -171,8 +187,34 @@ __device__ __forceinline__ void next_item(const TcWeights& p, const int* ne, Ite
     look(p, ne, t);
 }
 
-// kOne: items of one step.
-template <bool kOne>
+// This address in another CTA of the cluster; a store and an arrival there.
+__device__ __forceinline__ uint32_t peer_addr(const void* local, int rank) {
+    uint32_t d;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(d) : "r"(smem_u32(local)), "r"(rank));
+    return d;
+}
+__device__ __forceinline__ void peer_store(uint32_t addr, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+__device__ __forceinline__ void peer_arrive(uint32_t addr) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+// By every thread of every CTA of the cluster.
+__device__ __forceinline__ void cluster_meet() {
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// Steps that a call of `tiles` takes on `at_once` groups of C CTAs that share a tile;
+// meeting costs about three.
+__host__ __device__ __forceinline__ long cost_of(long tiles, long at_once, long steps, int C) {
+    return (tiles + at_once - 1) / at_once * ((steps + C - 1) / C + (C > 1 ? 3 : 0));
+}
+
+// kOne: items of one step.  kCluster: the 2^cshift CTAs of a cluster share an item, a run
+// of its steps each, and their sums meet in the first CTA's shared memory, in the CTAs'
+// order -- where the tiles that have entries (known here, not on the host) are done
+// sooner so; else each takes items of its own.
+template <bool kOne, bool kCluster>
 __global__ void __launch_bounds__(kThreads, 1)
 weights_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_q,
                   const __grid_constant__ TcWeights p) {
@@ -206,6 +248,7 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             mbar_init(&ctl->s_free[i], kOne ? kSumWarps / 2 : kSumWarps);
         }
         for (int i = 0; i < kXs; ++i) mbar_init(&ctl->x_full[i], kOne ? 4 : kSumWarps - 4);
+        for (int i = 0; i < kRounds; ++i) mbar_init(&ctl->c_full[i], kCluster ? 4 * ((1 << p.cshift) - 1) : 1);
         mbar_init(&ctl->fin, 1);
         mbar_init(&ctl->stall_bar, 1);
         // a CTA started after another one timed out does no work
@@ -221,15 +264,30 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, ctl->tmem_base, 0);
+    if (kCluster) {
+        if (warp == 0) {
+            int live = 0;                                // tiles with entries
+            for (int i = lane; i < a.B; i += 32)
+                live += ((i < kNe ? ctl->ne[i] : entries_of(a, i)) + kKeys - 1) / kKeys;
+            live = __reduce_add_sync(0xffffffffu, live);
+            if (lane == 0) ctl->cshift = cost_of(live, gridDim.x >> p.cshift, p.steps, 1 << p.cshift) <
+                                                 cost_of(live, gridDim.x, p.steps, 1) ? p.cshift : 0;
+        }
+        cluster_meet();                                  // (the peers' barriers are there, too)
+    }
+    const int shared = kCluster ? ctl->cshift : 0;
+    const int rank = (int)blockIdx.x & ((1 << shared) - 1);
+    const int s_lo = rank * p.steps >> shared, s_hi = (rank + 1) * p.steps >> shared;        // the CTA's steps
+    const Walk walk = walk_of(p, shared);
 
     // the CTA's live items
     const auto first_live = [&]() -> Item {
-        Item t = first_item(p, ctl->ne);
-        while (t.i < p.items && !t.live) next_item(p, ctl->ne, t);
+        Item t = first_item(p, walk, ctl->ne);
+        while (t.i < p.items && !t.live) next_item(p, walk, ctl->ne, t);
         return t;
     };
     const auto next_live = [&](Item& t) {
-        do next_item(p, ctl->ne, t);
+        do next_item(p, walk, ctl->ne, t);
         while (t.i < p.items && !t.live);
     };
     if (warp == kTmaWarp) {
@@ -249,7 +307,7 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 }
                 __syncwarp();
             }
-            for (int st = 0; st < p.steps; ++st, ++L) {
+            for (int st = s_lo; st < s_hi; ++st, ++L) {
                 const int sl = L % kStages;
                 if (L >= kStages) ok = wait(&ctl->freeb[sl], (L / kStages - 1) & 1);
                 ok = __all_sync(0xffffffffu, ok && !*abort);
@@ -316,10 +374,10 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             return true;
         };
         Item t = first_live();
-        int st = 0;
+        int st = s_lo;
         const auto advance = [&]() {
-            if (++st == p.steps) {
-                st = 0;
+            if (++st == s_hi) {
+                st = s_lo;
                 next_live(t);
             }
         };
@@ -385,7 +443,7 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         for (Item t = first_live(); t.i < p.items && ok; next_live(t)) {
             const int kb = k % kKBufs;
             ok = wait(&ctl->kfull[kb], (k / kKBufs) & 1);
-            for (int st = 0; st < p.steps && ok; ++st, ++L) {
+            for (int st = s_lo; st < s_hi && ok; ++st, ++L) {
                 const int sl = L % kStages, buf = L % kBufs;
                 ok = (L < kBufs || wait(&ctl->s_free[buf], (L / kBufs - 1) & 1)) && wait(&ctl->full[sl], (L / kStages) & 1);
                 if (!ok) break;
@@ -402,7 +460,7 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                     }
                     mma_commit(&ctl->freeb[sl]);
                     mma_commit(&ctl->s_full[buf]);
-                    if (st + 1 == p.steps) mma_commit(&ctl->kfree[kb]);
+                    if (st + 1 == s_hi) mma_commit(&ctl->kfree[kb]);
                 }
                 __syncwarp();
             }
@@ -433,10 +491,10 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             int s = a.idx ? (j < a.topk ? __ldg(a.idx + (size_t)t.b * a.topk + j) : -1) : j;
             if (s < 0 || s >= a.N_cap) s = -1;
             *had = 0.0f;
-            if (part_of == 0 && !a.idx && s >= 0 && a.in) *had = a.in[(size_t)t.b * a.N_cap + s];
+            if (part_of == 0 && rank == 0 && !a.idx && s >= 0 && a.in) *had = a.in[(size_t)t.b * a.N_cap + s];
             return s;
         };
-        Item tn = first_item(p, ctl->ne);
+        Item tn = first_item(p, walk, ctl->ne);
         float had_n = 0.0f;
         int s_n = tn.i < p.items ? entry(tn, &had_n) : -1;
         while (tn.i < p.items && ok) {
@@ -444,10 +502,10 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             const int s = s_n;
             const float had = had_n;
             float* dst = a.out + (size_t)t.b * a.N_cap + s;
-            next_item(p, ctl->ne, tn);
+            next_item(p, walk, ctl->ne, tn);
             if (tn.i < p.items) s_n = entry(tn, &had_n);
             if (!t.live) {
-                if (h == 0 && !a.idx && s >= 0) *dst = had;
+                if (h == 0 && rank == 0 && !a.idx && s >= 0) *dst = had;
                 continue;
             }
             if (kOne && (k & 1) != (h >> 1)) {
@@ -456,7 +514,7 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 continue;
             }
             float sum = 0.0f;
-            for (int st = 0; st < p.steps; ++st, ++L) {
+            for (int st = s_lo; st < s_hi; ++st, ++L) {
                 const int buf = L % kBufs;
                 // this thread's columns of the step: a quarter or half of 128 or 64
                 const int n = min(kCols, (p.cols - st * kCols + 63) & ~63) / share, c0 = n * part_of;
@@ -504,6 +562,20 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
 #pragma unroll
                 for (int q = 0; q < kQuarters - 1; ++q)
                     if (q < share - 1) sum += ctl->xs[k % kXs][q][r];
+                if (kCluster && shared) {
+                    const int others = (1 << shared) - 1;
+                    if (rank > 0) {
+                        peer_store(peer_addr(&ctl->cx[k * others + rank - 1][r], 0), sum);
+                        __syncwarp();
+                        if (lane == 0) peer_arrive(peer_addr(&ctl->c_full[k], 0));
+                        ++k;
+                        continue;
+                    }
+                    ok = wait(&ctl->c_full[k], 0);
+                    if (!ok) break;
+                    asm volatile("fence.acq_rel.cluster;" ::: "memory");
+                    for (int q = 0; q < others; ++q) sum += ctl->cx[k * others + q][r];
+                }
                 if (s >= 0) {
                     // (an entry listed twice receives its weight twice: equal terms, any order)
                     if (a.idx) atomicAdd(dst, sum);
@@ -517,6 +589,7 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (kCluster) cluster_meet();                        // (the first CTA's memory outlives the others' stores)
     if (warp == kMmaWarp) tmem_dealloc(tmem, kBufs * kCols);
 }
 
@@ -549,6 +622,59 @@ bool make_map_weights(CUtensorMap* m, const void* ptr, uint64_t rows, int n) {
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+cudaLaunchConfig_t cluster_config(int C, int clusters, cudaLaunchAttribute* attr) {
+    cudaLaunchConfig_t cfg = {};
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)C;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3((unsigned)(C * clusters));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cfg;
+}
+
+// Clusters of 2^cshift CTAs that run at once on the current device (0: unknown).
+int most_clusters(int cshift) {
+    static std::atomic<int> known[64][4];                    // plus one
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    if (const int k = known[dev][cshift].load(std::memory_order_relaxed)) return k - 1;
+    const auto kern = weights_tc_kernel<false, true>;
+    cudaLaunchAttribute attr[1];
+    const cudaLaunchConfig_t cfg = cluster_config(1 << cshift, 1, attr);
+    int n = 0;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    known[dev][cshift].store(n + 1, std::memory_order_relaxed);
+    return n;
+}
+
+// log2 of the CTAs of a cluster: one, or what suits a cache that is half full, where that
+// saves a quarter of the steps (a cluster's start costs about 2 us) and a full cache, on
+// as many CTAs as the clusters leave, takes no more.  64 query rows of 64 heads over
+// 2048 entries take 14 us, without clusters 27; over a cache of 16384 that holds half
+// as many 20, without 28; over a full one 31, without 28.
+int choose_cluster(int items, int steps) {
+    const long plain = cost_of((items + 1) / 2, kSms, steps, 1), full = cost_of(items, kSms, steps, 1);
+    long best = plain;
+    int shift = 0;
+    for (int k = 1; k <= 3 && (1 << k) <= steps; ++k) {
+        const int C = 1 << k, n = std::min(most_clusters(k), items);
+        if (n <= 0) continue;
+        const long rounds = (items + n - 1) / n, half = cost_of((items + 1) / 2, n, steps, C);
+        if (rounds > kRounds || rounds * (C - 1) > kCx || half >= best || 4 * half > 3 * plain) continue;
+        if (std::min(cost_of(items, n, steps, C), cost_of(items, (long)n * C, steps, 1)) > full) continue;
+        best = half;
+        shift = k;
+    }
+    return shift;
+}
+
 }  // namespace
 
 // Served here: bf16 rows of 128 channels.  (Lists with a single step of columns go
@@ -572,9 +698,9 @@ cudaError_t launch_entry_weights_tc(const WeightsArgs& a, uint32_t* err, cudaStr
     const long items = (long)(((a.idx ? a.topk : a.N_cap) + kKeys - 1) / kKeys) * a.B;
     if (items > (1L << 31) - 1 - kSms) return cudaErrorInvalidConfiguration;
     p.items = (int)items;
-    const int grid = (int)std::min<long>(items, kSms);
-    p.dchunk = grid / a.B;
-    p.db = grid % a.B;
+    p.cshift = a.idx ? 0 : choose_cluster(p.items, p.steps);
+    const int C = 1 << p.cshift;
+    const int groups = (int)std::min<long>(items, C == 1 ? kSms : most_clusters(p.cshift));
     const auto log2_of = [](int v) { return (v & (v - 1)) ? -1 : 31 - __builtin_clz((unsigned)v); };
     p.hshift = log2_of(a.H);
     p.mshift = log2_of(a.m);
@@ -582,10 +708,21 @@ cudaError_t launch_entry_weights_tc(const WeightsArgs& a, uint32_t* err, cudaStr
     p.err = err;
     p.wait_ns = wait_limit_ns();
     p.stall = take_stall();
-    const auto kern = p.steps == 1 ? weights_tc_kernel<true> : weights_tc_kernel<false>;
+    const auto kern = C > 1 ? weights_tc_kernel<false, true> : p.steps == 1 ? weights_tc_kernel<true, false> : weights_tc_kernel<false, false>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
     if (e != cudaSuccess) return e;
-    e = launch_dependent(kern, (unsigned)grid, kThreads, kSmem, s, tm_k, tm_q, p);
+    if (C > 1) {
+        cudaLaunchAttribute attr[2];
+        cudaLaunchConfig_t cfg = cluster_config(C, groups, attr);
+        cfg.stream = s;
+        attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[1].val.programmaticStreamSerializationAllowed = 1;
+        cfg.numAttrs = 2;
+        e = cudaLaunchKernelEx(&cfg, kern, tm_k, tm_q, p);
+        if (e != cudaSuccess) e = cudaGetLastError();
+    } else {
+        e = launch_dependent(kern, (unsigned)groups, kThreads, kSmem, s, tm_k, tm_q, p);
+    }
     count_launch();
     return e;
 }

@@ -549,6 +549,20 @@ def test_entry_weights_many_elements_and_steps(B, nq, N, topk):
         assert torch.equal(got, run_weights(a))
 
 
+@pytest.mark.parametrize("B,nq,H,N,fill", [
+    # few tiles of many steps (clusters of 8, 4 and 2 CTAs a tile), several rounds of them, caches
+    # that hold little and caches that are full, elements without entries
+    (1, 40, 64, 700, 1.0), (3, 24, 64, 900, 0.6), (1, 64, 64, 9000, 0.4), (1, 64, 64, 9000, 1.0), (2, 8, 128, 3000, 0.5),
+    (7, 16, 64, 1500, 0.3), (1, 5, 64, 129, 1.0), (40, 6, 64, 300, 0.9)])
+def test_entry_weights_of_tiles_shared_by_clusters(B, nq, H, N, fill):
+    a = weights_case(69 + nq, BF, B, nq, H, 128, N)
+    a["n_entries"] = i32([0 if b % 3 == 1 else max(1, int(N * fill) - 5 * b) for b in range(B)])
+    a["kv"][:, int(N * fill) + 1:] = math.nan              # nothing sees these
+    got = check_weights(a)
+    assert torch.equal(got, run_weights(a))
+    assert torch.equal(got[:, int(N * fill) + 1:], a["weight"][:, int(N * fill) + 1:])
+
+
 def test_prefix_workspace():
     a = prefix_case(66, BF, 3, 1, 64, 128, 900, 30, 100, m=4)
     want = run_prefix(a)
@@ -570,7 +584,8 @@ def test_prefix_workspace():
 def test_timeouts_are_reported_and_the_next_call_runs_clean():
     lib = api.load()
     a, w = prefix_case(67, BF, 70, 1, 64, 128, 700, 30, 100, m=4), weights_case(68, BF, 3, 2, 64, 128, 500)
-    for run in (lambda: run_prefix(a)[0], lambda: run_weights(w)):
+    many = weights_case(70, BF, 1, 40, 64, 128, 700)
+    for run in (lambda: run_prefix(a)[0], lambda: run_weights(w), lambda: run_weights(many)):
         api.csa_check_device_error()
         want = run()
         torch.cuda.synchronize()
