@@ -66,7 +66,6 @@ struct __align__(16) Ctrl {
     uint64_t fin, stall_bar;     // (stall_bar: a barrier that nothing completes, for tests)
     uint32_t tmem_base;
     int abort;
-    int cshift;                  // log2 of the CTAs that share an item in this call
 };
 constexpr size_t kSmem = 1024 + (kKBufs + kStages) * kTileBytes + sizeof(Ctrl);
 
@@ -204,16 +203,8 @@ __device__ __forceinline__ void cluster_meet() {
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 
-// Steps that a call of `tiles` takes on `at_once` groups of C CTAs that share a tile;
-// meeting costs about three.
-__host__ __device__ __forceinline__ long cost_of(long tiles, long at_once, long steps, int C) {
-    return (tiles + at_once - 1) / at_once * ((steps + C - 1) / C + (C > 1 ? 3 : 0));
-}
-
 // kOne: items of one step.  kCluster: the 2^cshift CTAs of a cluster share an item, a run
-// of its steps each, and their sums meet in the first CTA's shared memory, in the CTAs'
-// order -- where the tiles that have entries (known here, not on the host) are done
-// sooner so; else each takes items of its own.
+// of its steps each; their sums meet in the first CTA's shared memory, in the CTAs' order.
 template <bool kOne, bool kCluster>
 __global__ void __launch_bounds__(kThreads, 1)
 weights_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_q,
@@ -264,18 +255,8 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, ctl->tmem_base, 0);
-    if (kCluster) {
-        if (warp == 0) {
-            int live = 0;                                // tiles with entries
-            for (int i = lane; i < a.B; i += 32)
-                live += ((i < kNe ? ctl->ne[i] : entries_of(a, i)) + kKeys - 1) / kKeys;
-            live = __reduce_add_sync(0xffffffffu, live);
-            if (lane == 0) ctl->cshift = cost_of(live, gridDim.x >> p.cshift, p.steps, 1 << p.cshift) <
-                                                 cost_of(live, gridDim.x, p.steps, 1) ? p.cshift : 0;
-        }
-        cluster_meet();                                  // (the peers' barriers are there, too)
-    }
-    const int shared = kCluster ? ctl->cshift : 0;
+    if (kCluster) cluster_meet();                        // (the peers' barriers are there, too)
+    const int shared = kCluster ? p.cshift : 0;
     const int rank = (int)blockIdx.x & ((1 << shared) - 1);
     const int s_lo = rank * p.steps >> shared, s_hi = (rank + 1) * p.steps >> shared;        // the CTA's steps
     const Walk walk = walk_of(p, shared);
@@ -562,7 +543,7 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
 #pragma unroll
                 for (int q = 0; q < kQuarters - 1; ++q)
                     if (q < share - 1) sum += ctl->xs[k % kXs][q][r];
-                if (kCluster && shared) {
+                if (kCluster) {
                     const int others = (1 << shared) - 1;
                     if (rank > 0) {
                         peer_store(peer_addr(&ctl->cx[k * others + rank - 1][r], 0), sum);
@@ -654,22 +635,20 @@ int most_clusters(int cshift) {
     return n;
 }
 
-// log2 of the CTAs of a cluster: one, or what suits a cache that is half full, where that
-// saves a quarter of the steps (a cluster's start costs about 2 us) and a full cache, on
-// as many CTAs as the clusters leave, takes no more.  64 query rows of 64 heads over
-// 2048 entries take 14 us, without clusters 27; over a cache of 16384 that holds half
-// as many 20, without 28; over a full one 31, without 28.
+// log2 of the CTAs that share an item: where the tiles are so few that it saves a quarter
+// of the steps, the two or so that meeting costs included.  64 query rows of 64 heads over
+// 2048 entries take 13 us, without clusters 27; 64 of 128 heads over 8192 31 and 50.
+// (With fewer rounds than that at stake, a full cache of 16384 took 35 us for 28.)
 int choose_cluster(int items, int steps) {
-    const long plain = cost_of((items + 1) / 2, kSms, steps, 1), full = cost_of(items, kSms, steps, 1);
+    const long plain = (long)((items + kSms - 1) / kSms) * steps;
     long best = plain;
     int shift = 0;
     for (int k = 1; k <= 3 && (1 << k) <= steps; ++k) {
         const int C = 1 << k, n = std::min(most_clusters(k), items);
         if (n <= 0) continue;
-        const long rounds = (items + n - 1) / n, half = cost_of((items + 1) / 2, n, steps, C);
-        if (rounds > kRounds || rounds * (C - 1) > kCx || half >= best || 4 * half > 3 * plain) continue;
-        if (std::min(cost_of(items, n, steps, C), cost_of(items, (long)n * C, steps, 1)) > full) continue;
-        best = half;
+        const long rounds = (items + n - 1) / n, cost = rounds * ((steps + C - 1) / C + 2);
+        if (rounds > kRounds || rounds * (C - 1) > kCx || cost >= best || 4 * cost > 3 * plain) continue;
+        best = cost;
         shift = k;
     }
     return shift;
