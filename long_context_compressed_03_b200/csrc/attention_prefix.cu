@@ -16,10 +16,11 @@
 // rows.  Its list of key tiles (128 keys):
 //   - shared tiles: prefix entries that every row of the unit sees, by TMA;
 //   - own tiles: each of the G rows gets H columns, filled with that row's further
-//     keys (its window, the rest of the prefix it sees, its own entries); the
-//     other rows' weights there are zero.  Runs of 64 rows in one place come by
-//     TMA, the rest by 16-byte cp.async, rows past a list's end as zero rows, so
-//     nothing a row may not see is ever multiplied, whatever it holds.
+//     keys (its window, the rest of the prefix it sees, its own entries); P V
+//     updates each row's lanes from its own columns only (the other row's keys may
+//     be infinite or NaN, which a weight of zero would not take out).  Runs of 64
+//     rows in one place come by TMA, the rest by 16-byte cp.async, rows past a
+//     list's end as zero rows, so nothing that a row may not see enters its output.
 // The units' lists are dealt over the CTAs of one wave: CTA c of n takes the
 // part [c U / n, (c+1) U / n) of the U units laid end to end, each unit's tiles
 // cut in that proportion.  A unit that stays whole is written out by its CTA;
@@ -521,6 +522,7 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         bool ok = true;
         for (int u = u0; u < u1 && ok; ++u) {
             const int n = __shfl_sync(0xffffffffu, geo[u - u0].hi - geo[u - u0].lo, 0);
+            const int shared = __shfl_sync(0xffffffffu, geo[u - u0].P - geo[u - u0].lo, 0);   // (may be below 0)
             if (n == 0) continue;
             if (no > 0) ok = wait(&ctl->o_free, (no - 1) & 1);      // the previous part's O has been read
             ++no;
@@ -539,10 +541,21 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         tc_fence_after();
                         if (elect_one()) {
                             if (mode != kMax) {
+// (an own tile of two rows: each row's lanes with its own 64 keys)
+                                const bool own = G == 2 && i >= shared;
+                                const uint32_t pa = a + 64 * q;
+                                const uint64_t v = vd + (uint64_t)(4 * q * (2048 >> 4));
+                                if (own) {
 #pragma unroll
-                                for (int kk = 4 * q; kk < 4 * q + 4; ++kk)
-                                    mma_bf16_ts(tmem + kOCol, a + (kk >> 1) * 32 + (kk & 1) * 8,
-                                                vd + (uint64_t)(kk * (2048 >> 4)), id_pv, kk > 0 ? 1u : acc);
+                                    for (int kk = 0; kk < 4; ++kk)
+                                        mma_bf16_ts_half(tmem + kOCol, pa + (kk >> 1) * 32 + (kk & 1) * 8,
+                                                         v + (uint64_t)(kk * (2048 >> 4)), id_pv, kk > 0 ? 1u : acc, q);
+                                } else {
+#pragma unroll
+                                    for (int kk = 0; kk < 4; ++kk)
+                                        mma_bf16_ts(tmem + kOCol, pa + (kk >> 1) * 32 + (kk & 1) * 8,
+                                                    v + (uint64_t)(kk * (2048 >> 4)), id_pv, kk + q > 0 ? 1u : acc);
+                                }
                                 if (q == 1) {
                                     mma_commit(&ctl->freeb[slot]);
                                     mma_commit(&ctl->s_free[buf]);

@@ -239,6 +239,42 @@ def test_prefix_partial_visibility_empty_rows_and_poison(dt, H, D):
     check_prefix(a, dt)
 
 
+@pytest.mark.parametrize("nq", [1, 2])
+@pytest.mark.parametrize("where", ["own", "window", "rest of the prefix"])
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+def test_prefix_non_finite_keys_stay_with_the_rows_that_see_them(where, value, nq):
+    # 64 heads: two rows share the MMA's 128 lanes and an own tile holds 64 keys of each.  One key
+    # of one of the two is not finite; the row that does not see it keeps its result
+    B, Np, cap, W, m = 4, 300, 90, 100, 4
+    a = prefix_case(81 + nq, BF, B, nq, 64, 128, Np, cap, W, m=m)
+    a["n_entries"], last = i32([Np + 70, Np + 80, Np + 75, Np + 90]), i32([1490, 1507, 1499, 1567])
+    if where == "rest of the prefix":                # only row (0, 0) sees less than the whole prefix
+        a["n_entries"][0] = 140
+    a["q_pos"] = (last[:, None] - (nq - 1) * m + m * torch.arange(nq, device=DEV, dtype=torch.int32)).contiguous()
+    a["raw_pos0"] = (last - (a["kv_raw"].shape[1] - 1)).contiguous()
+    bad = [(1, j) for j in range(nq)]                # (the unit's other row: (0, 0), or for two rows an element (1, 0))
+    if where == "own":
+        vis = int((a["q_pos"][1, -1] + 1) // m)      # the entry that only element 1's last row sees
+        a["kv_c"][1, (min(vis, Np + 80) - Np - 1) if nq == 2 else 33] = value
+        bad = bad[-1:]
+    elif where == "window":
+        a["kv_raw"][1, -1 if nq == 2 else 7] = value
+        bad = bad[-1:]
+    else:
+        a["kv_p"][150] = value                       # (in a tile that has keys of both)
+        bad = [(b, j) for b in range(1, B) for j in range(nq)]
+    out, lse = run_prefix(a)
+    want, wl, bound, bl = ref.prefix_attention(a, BF, BF)
+    for b in range(B):
+        for j in range(nq):
+            if (b, j) in bad:
+                assert not bool(torch.isfinite(out[b, j].float()).any())
+                continue
+            assert bool(torch.isfinite(want[b, j]).all())
+            within(out[b, j], want[b, j], bound[b, j], f"row {b}, {j}")
+            within(lse[b, j], wl[b, j], bl[b, j], f"lse of row {b}, {j}")
+
+
 @pytest.mark.parametrize("H", [64, 128])
 def test_prefix_defaults_scale_and_large_scores(H):
     # no optional arrays (positions 0 .. n_q - 1: a prefill over a prefix of m = 1 entries), a given
