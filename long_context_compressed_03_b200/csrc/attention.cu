@@ -179,9 +179,10 @@ __global__ void __launch_bounds__(kThreads) attn_generic_kernel(AttnArgs a) {
                 l = fmaf(w, lc[k], l);
                 v = fmaf(w, oc[k], v);
             }
-            store_out<T>(static_cast<T*>(a.out) + (size_t)row * H * D + p, l > 0.0f ? v / l : 0.0f);
+            // (l = 0: no key; a key that holds NaN makes l NaN, and so the row)
+            store_out<T>(static_cast<T*>(a.out) + (size_t)row * H * D + p, l == 0.0f ? 0.0f : v / l);
             if (a.lse_out && c == 0)
-                a.lse_out[(size_t)row * H + ph] = l > 0.0f ? (M + log2f(l)) / kLog2e : -INFINITY;
+                a.lse_out[(size_t)row * H + ph] = l == 0.0f ? -INFINITY : (M + log2f(l)) / kLog2e;
         }
         cluster.sync();                  // the peers read this CTA's shared memory
         return;

@@ -275,6 +275,20 @@ def test_prefix_non_finite_keys_stay_with_the_rows_that_see_them(where, value, n
             within(lse[b, j], wl[b, j], bl[b, j], f"lse of row {b}, {j}")
 
 
+@pytest.mark.parametrize("dt,H,D", [(F32, 8, 64), (F32, 64, 128), (BF, 8, 128)])
+def test_prefix_a_visible_nan_is_not_an_empty_row(dt, H, D):
+    # clusters of CTAs a row: the key is one CTA's, the others' keys are finite
+    a = prefix_case(88, dt, 2, 1, H, D, 400, 20, 64)
+    a["kv_c"][1, 0] = math.nan
+    a["n_entries"], a["q_pos"] = i32([410, 410]), i32([[1700], [1700]])
+    a["raw_pos0"] = i32([1637, 1637])
+    out, lse = run_prefix(a)
+    want, wl, bound, bl = ref.prefix_attention(a, dt, BF if dt == BF else None)
+    within(out[0], want[0], bound[0], "the other element")
+    within(lse[0], wl[0], bl[0], "its lse")
+    assert bool(torch.isnan(out[1]).all()) and bool(torch.isnan(lse[1]).all())
+
+
 @pytest.mark.parametrize("H", [64, 128])
 def test_prefix_defaults_scale_and_large_scores(H):
     # no optional arrays (positions 0 .. n_q - 1: a prefill over a prefix of m = 1 entries), a given
