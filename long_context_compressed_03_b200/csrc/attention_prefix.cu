@@ -92,7 +92,9 @@ struct __align__(8) Ctrl {
     int abort;
     int q_ahead;             // the first unit's Q was requested in the prologue
     int over[3];             // (attempt mod 3) some sum of weights left the range
-    float m[kRows];          // offsets in use (base 2)
+    // offsets in use (base 2), by the parity of the CTA's units: the next unit's first tile
+    // may give its offsets while this unit's are still read for the LSE and the workspace
+    float m[2][kRows];
     float xm[4][kRows];      // per thread of a row: its maximum
     float xl[2][4][2][kRows];   // (by attempt parity) its sums of rounded / exact weights
 };
@@ -597,10 +599,11 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             const int own_len = row.n_pre + row.n_own + row.n_win;
             const int n = g.hi - g.lo;
             float l_r = 0.0f, l_e = 0.0f, m = -INFINITY;
+            float* offset = ctl->m[nm & 1];                      // (a unit adds one to nm)
             Mode mode = kFast;
             if (n > 0) do {
                 l_r = l_e = 0.0f;
-                m = mode == kExact ? ctl->m[r] : -INFINITY;
+                m = mode == kExact ? offset[r] : -INFINITY;
                 const bool leads = L_grp == L;               // this group has the attempt's first tile
                 bool have_m = mode != kFast;                 // kFast: m comes with the first tile
                 float top = -INFINITY;                       // kMax: largest score seen
@@ -640,13 +643,13 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                                 float z = tmem_ld1(my + buf * 128 + c0) * p.scale_log2;
                                 if (!(fabsf(z) < INFINITY)) z = 0.0f;
                                 if (i >= g.P && own_len <= (i - g.P) * H) z = -INFINITY;
-                                ctl->m[r] = z;
+                                offset[r] = z;
                                 __syncwarp();
                                 if (lane == 0) mbar_arrive(&ctl->m_ready);
                             }
                             ok = wait(&ctl->m_ready, nm & 1);
                             if (!ok) break;
-                            m = ctl->m[r];
+                            m = offset[r];
                             have_m = true;
                         }
                         // P over the S it is made from
@@ -710,7 +713,7 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 if (ok && was != kMax) ok = wait(&ctl->o_full, (no - 1) & 1);
                 if (ok && was == kMax) {
                     // (each of the row's four threads writes the same value)
-                    ctl->m[r] = max3(fmaxf(ctl->xm[0][r], ctl->xm[1][r]), ctl->xm[2][r], ctl->xm[3][r]);
+                    offset[r] = max3(fmaxf(ctl->xm[0][r], ctl->xm[1][r]), ctl->xm[2][r], ctl->xm[3][r]);
                     __syncwarp();
                 }
             } while (ok && mode != kFast);
@@ -725,7 +728,7 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     l_r += ctl->xl[(k - 1) & 1][q][0][r];
                     l_e += ctl->xl[(k - 1) & 1][q][1][r];
                 }
-                m = ctl->m[r];
+                m = offset[r];
             }
             if (!row.on) {               // no position: no key, whatever the shared tiles held
                 m = -INFINITY;

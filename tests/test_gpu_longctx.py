@@ -548,6 +548,25 @@ def test_prefix_with_more_units_than_ctas(B, nq, H):
     assert torch.equal(out, o2) and torch.equal(lse, l2)
 
 
+@pytest.mark.parametrize("H,Np", [(128, 128), (128, 300), (64, 128), (64, 384)])
+def test_prefix_units_that_follow_one_another_keep_their_offsets(H, Np):
+    # several units of one or three tiles a CTA (the two groups of softmax warps take the units'
+    # first tiles in turn), the scores of neighbouring rows far apart: a row's LSE and, where a
+    # unit is cut, its weight in the join go by the offset of its own unit
+    B = 1200
+    a = prefix_case(97, BF, B, 1, H, 128, Np, 0, 0)
+    a["q_pos"] = torch.full_like(a["q_pos"], 4 * Np + 3)
+    step = torch.arange(B, device=DEV) * 37 % 11 - 5
+    a["q"] = (a["q"].float() * 2.0 ** step[:, None, None, None]).to(BF)
+    a["kv_p"][0] = 1.0                                     # (the key that gives the offsets)
+    out, lse = run_prefix(a)
+    want, wl, bound, bl = ref.prefix_attention(a, BF, BF)
+    for _ in range(20):
+        within(out, want, bound, "prefix attention")
+        within(lse, wl, bl, "lse")
+        out, lse = run_prefix(a)
+
+
 def test_offsets_past_32_bits():
     # caches and heads whose last rows lie more than 2^31 elements in
     g, B, N = gen(64), 5, 4_000_000
