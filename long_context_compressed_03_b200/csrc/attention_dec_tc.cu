@@ -221,6 +221,41 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dec_tc_kernel(const __grid_c
     cg::cluster_group cluster = cg::this_cluster();
     const int C = (int)cluster.num_blocks();
     const int rank = (int)cluster.block_rank();
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    // What needs no global memory comes before the wait for the kernel launched just before
+    // this one (the indexer lets this grid start early, see launch_attention_dec_tc).  That
+    // kernel may have written any of the call's arrays: idx, but also q, the new window row or
+    // the positions (a rotation, an append), and its writes are sure to be visible only
+    // behind the wait.
+    if (tid == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&ctl->full[s], kLoadThreads);
+            mbar_init(&ctl->freeb[s], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&ctl->s_full[i], 1);
+            mbar_init(&ctl->p_ready[i], kSoftWarps);
+            mbar_init(&ctl->p_free[i], 1);
+        }
+        mbar_init(&ctl->pv_done, 1);
+        mbar_init(&ctl->o_done, 1);
+        mbar_init(&ctl->fin, 1);
+        mbar_init(&ctl->stall_bar, 1);
+        prefetch_tmap(&tm_c);
+        prefetch_tmap(&tm_w);
+        fence_barrier_init();
+    }
+    if (tid < kH) {
+        sM[tid] = -INFINITY;
+        sTmax[tid] = INT_MIN;
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(&ctl->tmem_base, 256);
+        tmem_relinquish();
+    }
+    grid_wait();
+    if (tid == 0) ctl->abort = (*reinterpret_cast<volatile uint32_t*>(err) != 0u) ? 1 : 0;
     const int row = blockIdx.y;
     const int b = row / a.n_q;
     const int t = a.q_pos ? a.q_pos[row] : a.pos0 + (row - b * a.n_q);
@@ -231,7 +266,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dec_tc_kernel(const __grid_c
     const int ntile = rank < NT ? (NT - rank + C - 1) / C : 0;
     // this CTA's tile j is the row's tile rank + (ntile - 1 - j) C: the window tiles first
     auto kk0_of = [&](int j) { return (rank + (ntile - 1 - j) * C) * kBN; };
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     volatile int* abort = &ctl->abort;
     const float sl2 = a.scale * kLog2e;
     const int hmax = (kH + C - 1) / C;                      // heads a CTA finalises, at most
@@ -260,37 +294,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dec_tc_kernel(const __grid_c
         tma_load_2d(dst0 + kHalfK, m, 64, y, bar);
     };
 
-    if (tid == 0) {
-        for (int s = 0; s < kStages; ++s) {
-            mbar_init(&ctl->full[s], kLoadThreads);
-            mbar_init(&ctl->freeb[s], 1);
-        }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&ctl->s_full[i], 1);
-            mbar_init(&ctl->p_ready[i], kSoftWarps);
-            mbar_init(&ctl->p_free[i], 1);
-        }
-        mbar_init(&ctl->pv_done, 1);
-        mbar_init(&ctl->o_done, 1);
-        mbar_init(&ctl->fin, 1);
-        mbar_init(&ctl->stall_bar, 1);
-        ctl->abort = (*reinterpret_cast<volatile uint32_t*>(err) != 0u) ? 1 : 0;
-        fence_barrier_init();
-    }
-    if (tid < kH) {
-        sM[tid] = -INFINITY;
-        sTmax[tid] = INT_MIN;
-    }
-    if (warp == kMmaWarp) {
-        tmem_alloc(&ctl->tmem_base, 256);
-        tmem_relinquish();
-    }
     __syncthreads();
     // the first contiguous tiles and Q need no row codes: start them now
     // (nothing is started when an earlier launch left the error word set)
     if (tid == 0 && !*abort) {
-        prefetch_tmap(&tm_c);
-        prefetch_tmap(&tm_w);
         for (int j = 0; j < lead; ++j)
             if (tile_kind(j)) issue_tma(j);
     }
@@ -304,11 +311,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dec_tc_kernel(const __grid_c
         }
         asm volatile("cp.async.commit_group;" ::: "memory");          // Q: the oldest group
     }
-    // The indices may come from the kernel launched just before this one (the
-    // indexer lets this grid start early, see launch_attention_dec_tc): wait
-    // for it before the first read of idx.  Everything above reads only the
-    // caller's inputs, never a preceding kernel's output.
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     // ---- row codes: >= 0 physical row of a compressed entry, <= -2 raw row -(code + 2), -1 none
     for (int i = tid; i < ntile * kBN; i += kThreads) {
         const int kk = kk0_of(i / kBN) + (i % kBN);
@@ -770,9 +772,9 @@ cudaError_t launch_attention_dec_tc(const AttnArgs& a, uint32_t* err, cudaStream
     cfg.dynamicSmemBytes = L.bytes;
     cfg.stream = s;
     // Programmatic stream serialisation: when the kernel before this one
-    // (the decode indexer) signals early, this grid launches and runs its
-    // prologue -- TMEM, barriers, Q and the first window tiles -- while that
-    // kernel finishes; griddepcontrol.wait orders the read of idx after it.
+    // (the decode indexer) signals early, this grid launches and sets up its
+    // barriers and TMEM while that kernel finishes; griddepcontrol.wait orders
+    // everything that reads the call's arrays after it.
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = (unsigned)C;

@@ -478,6 +478,51 @@ def test_a_shared_prefix_step_with_weights_of_the_own_entries():
     assert float((total - 64).abs().max()) <= 64 * 1e-4
 
 
+@pytest.mark.parametrize("call", ["hca", "csa"])
+def test_decode_attention_directly_behind_the_kernel_that_writes_its_inputs(call):
+    # the rotation writes q and the window row in place, the attention follows at once: eagerly and
+    # in a graph, with other inputs every time
+    g, B, N, W, steps = gen(101), 16, 300, 128, 24
+    raw = [normal(g, BF, B, 1, 64, 128) for _ in range(steps)]
+    rows = [normal(g, BF, B, 1, 1, 128) for _ in range(steps)]
+    kv, win = normal(g, BF, B, N, 128), normal(g, BF, B, W, 128)
+    pos, p0 = i32([[4 * N + 50]] * B), i32([4 * N + 50 - W + 1] * B)
+    idx = torch.rand(B, 1, N, generator=g, device=DEV).argsort(2)[:, :, :64].to(torch.int32).contiguous()
+    freqs, _ = api.rope_freqs(64)
+    q, row = torch.empty_like(raw[0]), torch.empty_like(rows[0])
+
+    def attend():
+        kw = dict(raw_pos0=p0, q_pos=pos)
+        if call == "hca":
+            return api.hca_attn(q, kv, 4, win, W, **kw)
+        return api.sparse_attn(q, kv, idx, win, W, **kw)
+
+    want = []
+    for k in range(steps):
+        api.csa_rope(raw[k], q, freqs, y=rows[k], y_out=row, pos=pos)
+        win[:, -1:] = row[:, 0]
+        torch.cuda.synchronize()
+        want.append(attend())
+        torch.cuda.synchronize()
+    win_y = win[:, -1].view(B, 1, 1, 128)                  # the new row's place in the window
+
+    def step(k):
+        api.csa_rope(raw[k], q, freqs, y=rows[k].view(B, 1, 1, 128), y_out=win_y, pos=pos)
+        return attend()
+
+    for _ in range(3):
+        got = [step(k) for k in range(steps)]
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = [step(k) for k in range(steps)]
+    for _ in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
 # ------------------------------------------------------------------ streams and graphs
 def _ops(a, w, weight):
     out, lse = run_prefix(a)

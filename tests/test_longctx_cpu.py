@@ -2,7 +2,10 @@
 points: what they refuse before anything reaches the GPU, and the frequency rule.
 CPU only: every call fails validation, is a no-op, or runs on the host."""
 import ctypes
+import glob
 import math
+import os
+import re
 
 import pytest
 import torch
@@ -199,6 +202,28 @@ def test_injected_launch_failures_surface(lib):
         assert lib.csa_debug_inject_launch_error(719) == OK
         assert call() == api.CSA_ERR_CUDA
     assert lib.csa_evict(FAKE, 0, 50, None, 10, 2, FAKE, None, None) == OK
+
+
+def test_dependent_kernels_wait_before_they_read_an_array():
+    # a kernel launched while the one before it ends sees that one's writes only behind its wait:
+    # what stands above it in the source sets up shared memory, barriers and TMEM
+    reads = re.compile(r"\ba\.\w+ ?\[|\ba\.\w+ \+|__ldg|row_keys\(|cp_async16\(|tma_load|load_q\(|\berr\)|issue_tma\((?!int)"
+                       r"|fill_\w+[<(]|entries_of\(")
+    waiting = 0
+    for path in sorted(glob.glob(os.path.join(build_mod.CSRC, "*.cu"))):
+        text = re.sub(r"//[^\n]*", "", open(path, encoding="utf-8").read())
+        for kernel in re.split(r"__global__", text)[1:]:
+            body = kernel[kernel.index("{"):]
+            end = re.search(r"\n}", body)
+            body = body[:end.start()] if end else body
+            at = re.search(r"grid_wait\(\)|griddepcontrol\.wait", body)
+            if at is None:
+                continue
+            waiting += 1
+            head = re.sub(r"auto \w+ = \[&\].*?\n    };", "", body[:at.start()], flags=re.S)    # (defined, called later)
+            early = reads.search(head)
+            assert early is None, (os.path.basename(path), early.group(0))
+    assert waiting >= 12
 
 
 def test_binding_checks_shapes():
