@@ -292,6 +292,8 @@ bool vec_supported(const RopeArgs& a) {
     return true;
 }
 
+constexpr int kMostPairs = 4096;                             // angles a CTA keeps: 32 KB
+
 // Cuts a call whose rows have rot_items and pass_items.
 RopeGrid cut(const RopeArgs& a, int rot_items, int pass_items, long most, long* blocks) {
     const long total = (long)a.B * a.n;
@@ -305,7 +307,7 @@ RopeGrid cut(const RopeArgs& a, int rot_items, int pass_items, long most, long* 
                                          std::min<long>(total * R / (16 * 148), most * pass));
     RopeGrid g{1, R, 1, ipr, step, 0.0f, 0.0f, {0.0f, 0.0f}, 0.0f};
     if (want >= R) {
-        g.tpb = std::max(1, std::min(want / R, 4096 / (a.d_rot / 2)));    // angles: 32 KB at most
+        g.tpb = std::max(1, std::min(want / R, kMostPairs / (a.d_rot / 2)));
     } else {
         g.chunks = (R + want - 1) / want;
         g.rpb = (R + g.chunks - 1) / g.chunks;
@@ -322,6 +324,17 @@ RopeGrid cut(const RopeArgs& a, int rot_items, int pass_items, long most, long* 
 size_t angle_bytes(const RopeArgs& a, const RopeGrid& g) {
     return (size_t)g.tpb * (a.d_rot / 2) * sizeof(float2) + g.tpb * sizeof(int);
 }
+// A kernel's shared memory goes with the call's sizes, the limit set for it does not: it is
+// the kernel's, so that of a smaller call on another host thread would hold for a larger
+// one that is about to be launched.  (Tokens a CTA: kMostPairs at most, at one pair each.)
+constexpr size_t kAngleLimit = kMostPairs * (sizeof(float2) + sizeof(int));
+constexpr size_t kTileLimit = 32768;                         // of rope_staged_kernel
+
+template <typename K>
+cudaError_t allow_smem(K* kern, size_t limit, size_t smem) {
+    if (smem > limit) return cudaErrorInvalidValue;
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)limit);
+}
 // In place, the channels that are not rotated are already there.
 int pass_channels(const RopeArgs& a) {
     const bool in_place = (!a.H[0] || a.x[0] == a.out[0]) && (!a.H[1] || a.x[1] == a.out[1]);
@@ -334,9 +347,9 @@ cudaError_t launch_vec(const RopeArgs& a, cudaStream_t s) {
     long blocks;
     const RopeGrid g = cut(a, (a.interleaved ? a.d_rot : a.d_rot / 2) / V, pass_channels(a) / V, 8, &blocks);
     if (blocks > (1L << 31) - 1) return cudaErrorInvalidConfiguration;
-    const size_t smem = (a.interleaved ? ring_bytes<false>() : ring_bytes<true>()) + angle_bytes(a, g);
+    const size_t ring = a.interleaved ? ring_bytes<false>() : ring_bytes<true>(), smem = ring + angle_bytes(a, g);
     auto kern = a.interleaved ? rope_vec_kernel<T, false> : rope_vec_kernel<T, true>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = allow_smem(kern, ring + kAngleLimit, smem);
     if (e != cudaSuccess) return e;
     e = launch_dependent(kern, (unsigned)blocks, kThreads, smem, s, a, g);
     count_launch();
@@ -405,10 +418,10 @@ bool staged_supported(const RopeArgs& a) {
 template <typename T>
 cudaError_t launch_staged(const RopeArgs& a, cudaStream_t s) {
     long blocks;
-    const RopeGrid g = cut(a, a.D / (16 / (int)sizeof(T)), 0, 2, &blocks);    // (a tile: 32 KB at most)
+    const RopeGrid g = cut(a, a.D / (16 / (int)sizeof(T)), 0, 2, &blocks);    // (a tile: kTileLimit at most)
     if (blocks > (1L << 31) - 1) return cudaErrorInvalidConfiguration;
     const size_t smem = (size_t)g.tpb * g.rpb * a.D * sizeof(T) + angle_bytes(a, g);
-    cudaError_t e = cudaFuncSetAttribute(rope_staged_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = allow_smem(rope_staged_kernel<T>, kTileLimit + kAngleLimit, smem);
     if (e != cudaSuccess) return e;
     e = launch_dependent(rope_staged_kernel<T>, (unsigned)blocks, kThreads, smem, s, a, g);
     count_launch();

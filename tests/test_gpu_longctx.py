@@ -1,6 +1,7 @@
 """Rotary positions, shared-prefix attention, entry weights and eviction on the
 GPU, against their definitions in 64 bits (longctx_ref)."""
 import math
+import threading
 
 import pytest
 import torch
@@ -124,6 +125,36 @@ def test_rope_gradient():
         assert abs(diff - float(grad.view(-1)[k])) <= 4 * 4 * (4.6e-7 * 12 * 1.14 + 2.0 ** -22)
     back, _ = api.rope(api.rope(x, freqs, pos=pos)[0], freqs, pos=pos, transpose=True)
     assert float((back - x).abs().max()) <= 2 * 2 * 4.6e-7 * 12           # scale 1: the inverse
+
+
+def test_rope_from_several_host_threads():
+    # calls whose CTAs need different amounts of shared memory, at the same time
+    lib, calls = api.load(), []
+    for k, (shape, rot) in enumerate((((1, 32768, 1, 128), 64), ((64, 1, 65, 128), 64), ((1, 9000, 1, 80), 50),
+                                      ((3, 1, 17, 80), 50))):
+        B, n, H, D = shape
+        x, freqs = normal(gen(91 + k), BF, *shape), api.rope_freqs(rot)[0]
+        out, s = torch.empty_like(x), torch.cuda.Stream()
+        args = (x.data_ptr(), out.data_ptr(), H, None, None, None, 0, None, api.DT_BF16, B, n, D, rot, 0, 0,
+                freqs.data_ptr(), 1.0, None, 0, 1, 0, s.cuda_stream)
+        calls.append((args, x, freqs, out, s, api.rope(x, freqs, interleaved=False)[0]))
+    torch.cuda.synchronize()
+    start, failed = threading.Barrier(len(calls)), [0] * len(calls)
+
+    def work(k):
+        args, f = calls[k][0], lib.csa_rope
+        start.wait()
+        for _ in range(20000):
+            failed[k] += f(*args) != api.CSA_OK
+
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(len(calls))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert failed == [0] * len(calls)
+    assert all(torch.equal(c[3], c[5]) for c in calls)
 
 
 # ------------------------------------------------------------------ shared prefix
