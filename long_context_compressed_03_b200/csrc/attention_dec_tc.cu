@@ -685,7 +685,7 @@ bool make_map_dec(CUtensorMap* m, const void* ptr, uint64_t rows) {
 template <bool LSE>
 cudaError_t prepare(int C, size_t smem) {
     auto kern = attn_dec_tc_kernel<LSE>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = grow_smem_limit(kern, smem);
     if (e == cudaSuccess && C > 8) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     return e;
 }

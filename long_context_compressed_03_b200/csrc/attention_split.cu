@@ -418,7 +418,7 @@ cudaError_t launch_hd(const AttnArgs& a, cudaStream_t s) {
     const size_t smem = Plan<D>::kRingBytes + (size_t)H * D * 2 + sizeof(RowState) * H + sizeof(int) * max_chunk +
                         sizeof(uint32_t) * (max_chunk / 32);
     auto kern = attn_split_kernel<H, D>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = grow_smem_limit(kern, smem);
     if (e != cudaSuccess) return e;
     if (C > 8) {
         e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);

@@ -1,5 +1,6 @@
 // common.cuh -- device helpers shared by the CSA/HCA kernels (sm_100a).
 #pragma once
+#include <mutex>
 #include <utility>
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
@@ -65,6 +66,19 @@ __device__ __forceinline__ void store_out<__nv_bfloat16>(__nv_bfloat16* p, float
 __device__ __forceinline__ float relu0(float x) { return x > 0.0f ? x : 0.0f; }
 
 __device__ __forceinline__ int clampi(int v, int lo, int hi) { return v < lo ? lo : (v > hi ? hi : v); }
+
+// Lets a kernel have `bytes` of dynamic shared memory.  The limit is the kernel's, not the
+// launch's: it only grows, under a lock, since another host thread may be about to launch the
+// same kernel with more.
+template <typename... P>
+cudaError_t grow_smem_limit(void (*kern)(P...), size_t bytes) {
+    static std::mutex mu;
+    std::lock_guard<std::mutex> lock(mu);
+    cudaFuncAttributes now;
+    const cudaError_t e = cudaFuncGetAttributes(&now, kern);
+    if (e != cudaSuccess || (size_t)now.maxDynamicSharedSizeBytes >= bytes) return e;
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
 
 // A launch that may be set up while the kernel before it in the stream finishes (nothing
 // is triggered early: only the gap between the two goes).  The kernel calls grid_wait()

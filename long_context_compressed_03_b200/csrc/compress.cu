@@ -654,7 +654,7 @@ cudaError_t launch_stream_r(const CompressKArgs& a, cudaStream_t s) {
     sa.err = err;
     sa.wait_ns = wait_limit_ns();
     auto kern = compress_stream_kernel<R, OUT>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L.bytes);
+    cudaError_t e = grow_smem_limit(kern, L.bytes);
     if (e != cudaSuccess) return e;
     int dev = 0, sms = 148;
     if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
@@ -694,7 +694,7 @@ cudaError_t launch_mma_r(const CompressKArgs& a, cudaStream_t s) {
     const int G = a.m / R;
     const MmaSmem L = mma_smem(a.d_in, a.d_out, G, E + (a.overlap ? 1 : 0));
     auto kern = compress_mma_kernel<R, OUT>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L.bytes);
+    cudaError_t e = grow_smem_limit(kern, L.bytes);
     if (e != cudaSuccess) return e;
     dim3 grid((a.N_c + E - 1) / E, a.B);
     kern<<<grid, kThreads, L.bytes, s>>>(a, E);
@@ -727,7 +727,7 @@ cudaError_t launch_t(const CompressArgs& args, cudaStream_t s) {
     const size_t smem = sizeof(float) * ((size_t)(2 * kTile + 1) * a.d_in + (size_t)kKC * 128 +
                                          (size_t)kTile * a.d_out);
     auto kern = compress_kernel<Tin, OUT>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = grow_smem_limit(kern, smem);
     if (e != cudaSuccess) return e;
     dim3 grid((a.N_c + kTile - 1) / kTile, a.B);
     kern<<<grid, kThreads, smem, s>>>(a);

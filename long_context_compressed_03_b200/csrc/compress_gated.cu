@@ -240,7 +240,7 @@ cudaError_t launch_t(const GatedArgs& a, cudaStream_t s) {
     const int TE = tile_entries(a.m, a.overlap);
     const size_t smem = gated_smem<Tin>(a.d_in, a.d_out, TE);
     auto kern = compress_gated_kernel<Tin, OUT>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = grow_smem_limit(kern, smem);
     if (e != cudaSuccess) return e;
     dim3 grid((unsigned)((a.N_c + TE - 1) / TE), (unsigned)a.B);
     kern<<<grid, kThreads, smem, s>>>(a);

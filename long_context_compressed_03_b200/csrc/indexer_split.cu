@@ -469,7 +469,7 @@ cudaError_t launch_t(const IndexerArgs& a, cudaStream_t s) {
     const int C = choose_cluster(a);
     const size_t smem = sizeof(unsigned) * ((size_t)chunk_cap(a, C) + 2 * 256 + (PAGED ? kPageSlots : 0));
     auto kern = indexer_split_kernel<QD, NU, PAGED>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = grow_smem_limit(kern, smem);
     if (e != cudaSuccess) return e;
     if (C > 8) {
         e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);

@@ -227,7 +227,7 @@ template <int QD, int KD>
 cudaError_t launch_t(const IndexerArgs& a, cudaStream_t s) {
     const size_t smem = sizeof(unsigned) * (size_t)a.N_cap;
     auto kern = indexer_topk_kernel<QD, KD>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = grow_smem_limit(kern, smem);
     if (e != cudaSuccess) return e;
     kern<<<(unsigned)(a.B * a.n_q), kThreads, smem, s>>>(a);
     count_launch();

@@ -320,6 +320,35 @@ def test_prefix_a_visible_nan_is_not_an_empty_row(dt, H, D):
     assert bool(torch.isnan(out[1]).all()) and bool(torch.isnan(lse[1]).all())
 
 
+def test_attention_from_several_host_threads():
+    # the cluster-split kernel's shared memory goes with the keys a CTA has
+    lib, calls = api.load(), []
+    for k, (B, Np, cap) in enumerate(((2, 30, 5), (60, 9000, 9), (1, 700, 20), (111, 2000, 3))):
+        a = prefix_case(141 + k, BF, B, 1, 16, 64, Np, cap, 8)
+        out, s = torch.empty_like(a["q"]), torch.cuda.Stream()
+        ptr = {n: a[n].data_ptr() for n in ("q", "kv_p", "kv_c", "n_entries", "kv_raw", "raw_pos0", "raw_len", "q_pos")}
+        args = (ptr["q"], api.DT_BF16, B, 1, 16, 64, ptr["kv_p"], Np, ptr["kv_c"], cap, ptr["n_entries"], 4, ptr["kv_raw"],
+                8, ptr["raw_pos0"], ptr["raw_len"], 8, ptr["q_pos"], 0.0, out.data_ptr(), None, None, 0, s.cuda_stream)
+        calls.append((args, a, out, s, run_prefix(a)[0]))
+    torch.cuda.synchronize()
+    start, failed = threading.Barrier(len(calls)), [0] * len(calls)
+
+    def work(k):
+        args, f = calls[k][0], lib.hca_dense_attn_prefix
+        start.wait()
+        for _ in range(4000):
+            failed[k] += f(*args) != api.CSA_OK
+
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(len(calls))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert failed == [0] * len(calls)
+    assert all(torch.equal(c[2], c[4]) for c in calls)
+
+
 @pytest.mark.parametrize("H", [64, 128])
 def test_prefix_defaults_scale_and_large_scores(H):
     # no optional arrays (positions 0 .. n_q - 1: a prefill over a prefix of m = 1 entries), a given
