@@ -521,19 +521,9 @@ def _token_strides(t: torch.Tensor, name: str):
 
 
 def _rope_strides(x: torch.Tensor, out: torch.Tensor, name: str):
-    """{token, head} strides of x and of out."""
-    B, n, H, D = x.shape
-    st, spans = [], []
-    for t in (x, out):
-        s1, s2 = _token_strides(t, name)
-        st += [s1, s2]
-        e = t.element_size()
-        spans.append((t.data_ptr(), t.data_ptr() + ((B * n - 1) * s1 + (H - 1) * s2 + D) * e))
-    (a0, a1), (b0, b1) = spans
-    if a0 != b0 and a0 < b1 and b0 < a1 and x.numel():
-        # (views that interleave inside one buffer are refused too)
-        raise ValueError(f"the output of {name} overlaps it (give {name} itself to rotate in place)")
-    return _STRIDES(*st)
+    """{token, head} strides of x and of out.  (The library refuses outputs that share elements
+    with an input.)"""
+    return _STRIDES(*_token_strides(x, name), *_token_strides(out, name))
 
 
 def _rope_tensor(x: torch.Tensor | None, out: torch.Tensor | None, B: int, n: int, D: int, dt, name: str,

@@ -106,6 +106,20 @@ def test_rope_strided_views_and_default_positions(dt, D, extra):
     assert torch.equal(same.view(torch.uint8), v.view(torch.uint8))           # passed on bit for bit
 
 
+def test_rope_into_a_view_between_its_input():
+    # heads 2 and 3 of a buffer's five receive the rotation of heads 0 and 1
+    g, B, n = gen(95), 2, 9
+    buf = normal(g, BF, B, n, 5, 64)
+    freqs, _ = api.rope_freqs(32)
+    rest, want = buf[:, :, 4].clone(), api.rope(buf[:, :, :2], freqs, pos0=3)[0]
+    first = buf[:, :, :2].clone()
+    api.csa_rope(buf[:, :, :2], buf[:, :, 2:4], freqs, pos0=3)
+    assert torch.equal(buf[:, :, 2:4], want) and torch.equal(buf[:, :, :2], first) and torch.equal(buf[:, :, 4], rest)
+    for bad in (buf[:, :, 1:3], buf[:, 1:, :2]):           # outputs that share elements with their input
+        with pytest.raises((api.CsaError, ValueError)):
+            api.csa_rope(buf[:, :bad.shape[1], :2], bad, freqs)
+
+
 def test_rope_gradient():
     # the transposed call is the gradient of the rotation: against central differences of
     # sum(w * rope(x)), which is linear in x, so a difference over any step is exact up to rounding

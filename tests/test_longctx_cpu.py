@@ -91,6 +91,15 @@ def test_rope_refuses_tensors_that_overlap(lib):
     assert launched(p(0), p(0), p(256), p(256), fused, fused, n=1)
 
 
+def test_rope_strides_of_views_that_interleave():
+    # (the memory between a view's heads may be the other view's: no refusal of its own here)
+    buf = torch.zeros(2, 9, 5, 64)
+    assert list(api._rope_strides(buf[:, :, :2], buf[:, :, 2:4], "x")) == [320, 64, 320, 64]
+    assert list(api._rope_strides(buf[:, :, :1], torch.zeros(2, 9, 1, 64), "x")) == [320, 64, 64, 64]
+    with pytest.raises(ValueError, match="n tokens apart"):
+        api._rope_strides(buf[:, 1:], buf[:, 1:], "x")
+
+
 def test_binding_refuses_other_devices(monkeypatch):
     class Other:                                           # a tensor of device 1, as the binding sees it
         is_cuda, device, dtype, shape = True, "cuda:1", torch.float32, torch.Size((2, 4))
