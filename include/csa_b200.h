@@ -437,8 +437,8 @@ csa_status_t hca_dense_attn_at(const void* q, int dt, int B, int n_q, int H, int
  *     an attention output is turned back by the query's position).
  * The other channels are passed on unchanged.  A token with a negative
  * position has no place in the sequence: its heads are passed on unrotated.
- * Rotation runs in fp32 from angles exact to 2^-31 of a turn at any position,
- * and is rounded once.
+ * Rotation runs in fp32 from angles within 2^-27 of a turn of p * freqs[j], at any
+ * position and for any frequency allowed, and is rounded once.
  *
  *   x, y   up to two tensors with D channels a head, H and H_y heads a token
  *          (query heads and the KV row, say), rotated in one launch; H or H_y

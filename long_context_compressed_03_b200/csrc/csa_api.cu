@@ -631,6 +631,21 @@ static bool apart(const void* p, long sp, long ep, const void* q, long sq, long 
     return d >= ep && d + eq <= sp;
 }
 
+// f radians as a fraction of a turn (whole turns drop out), times 2^64, to the nearest: the
+// product of f's 53 bits and 2^128 / (2 pi), in integers, so that large f keep their fraction.
+// |f| < 2^20.
+static uint64_t turn_of(double f) {
+    using u128 = unsigned __int128;
+    const uint64_t c1 = 0x28be60db9391054aull, c0 = 0x7f09d5f47d4d3770ull;      // floor(2^128 / (2 pi))
+    int e = 0;
+    const uint64_t m = (uint64_t)std::ldexp(std::frexp(std::fabs(f), &e), 53);  // |f| = m 2^(e - 53)
+    const u128 top = (u128)m * c1 + (((u128)m * c0) >> 64);                     // the product without its low 64 bits
+    const int shift = 53 - e;                                                   // turn 2^64 = top / 2^shift; 33 at least
+    if (shift >= 128) return 0;
+    const uint64_t t = (uint64_t)(top >> shift) + (uint64_t)((top >> (shift - 1)) & 1u);
+    return f < 0.0 ? 0ull - t : t;
+}
+
 csa_status_t csa_rope(const void* x, void* x_out, int H, const long long* x_strides,
                       const void* y, void* y_out, int H_y, const long long* y_strides, int dt,
                       int B, int n, int D, int d_rot, int rot_offset, int interleaved,
@@ -697,14 +712,9 @@ csa_status_t csa_rope(const void* x, void* x_out, int H, const long long* x_stri
                     apart(os[w], a.os[w][0], ext[w][1], os[1 - w], a.os[1 - w][0], ext[1 - w][1], total, size),
                 "%s: the output of %s overlaps the other tensor", name, w ? "y" : "x");
     }
-    // frequencies as 64-bit fractions of a turn (whole turns drop out)
-    const long double inv_two_pi = 0.159154943091895335768883763372514362L;
     for (int j = 0; j < d_rot / 2; ++j) {
         REQUIRE(std::isfinite(freqs[j]) && std::fabs(freqs[j]) <= 1e6, "%s: freqs[%d] is not finite or above 10^6", name, j);
-        long double turn = (long double)freqs[j] * inv_two_pi;
-        turn -= floorl(turn);
-        const long double f = turn * 18446744073709551616.0L;
-        a.turn[j] = f >= 18446744073709551615.0L ? 0ull : (uint64_t)(f + 0.5L);
+        a.turn[j] = turn_of(freqs[j]);
     }
     a.dt = dt;
     a.B = B;

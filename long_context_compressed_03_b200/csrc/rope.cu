@@ -8,10 +8,12 @@
 //
 // The angle.  p * f reaches 10^6 rad at long contexts, where an fp32 product
 // is off by 0.06 rad.  The host turns f_j into a 64-bit fraction of a turn,
-// F = frac(f / 2 pi) * 2^64 (rounded in extended precision); p * F mod 2^64
-// is then the exact phase of the rounded frequency, whole turns dropping out
-// by overflow, for any integer p.  Its top 32 bits feed sincospi: the angle
-// is within 2^-32 turns + 2^53 relative of the exact one.
+// F = frac(f / 2 pi) * 2^64 (to the nearest, from 1 / 2 pi to 128 bits); p * F mod
+// 2^64 is then the exact phase of the rounded frequency, whole turns dropping out by
+// overflow, for any integer p: within 2^-34 of a turn of p * f where p < 2^31.  The
+// nearest quarter turn comes off in integers; the rest, at most 1/8 turn, is cut to 34
+// fraction bits and rounded to fp32 (2^-28 of a turn at most, less the closer it is to
+// the quarter turn) and feeds sincospi.  So the angle is within 2^-27 of a turn.
 #include <algorithm>
 
 #include "common.cuh"
@@ -32,10 +34,19 @@ __device__ __forceinline__ void fill_angles(const RopeArgs& a, long tok0, int n_
         const long tok = tok0 + t;
         const long p = a.pos ? (long)a.pos[tok] : a.pos0 + (tok % a.n) * (long)a.pos_step;
         const uint64_t phase = (uint64_t)p * a.turn[j];
-        // the top 32 bits as a signed fraction of a turn in [-1/2, 1/2), in units of pi
-        const float x = (float)(int32_t)(phase >> 32) * 0x1p-31f;
+        const uint32_t quarter = (uint32_t)((phase + (1ull << 61)) >> 62);
+        const int64_t rest = (int64_t)(phase - ((uint64_t)quarter << 62));       // [-1/8, 1/8) turn
         float s, c;
-        sincospif(x, &s, &c);
+        sincospif((float)(int32_t)(rest >> 30) * 0x1p-33f, &s, &c);              // in units of pi
+        if (quarter & 1u) {                                  // (a quarter turn on: cos is -sin, sin is cos)
+            const float w = c;
+            c = -s;
+            s = w;
+        }
+        if (quarter & 2u) {
+            c = -c;
+            s = -s;
+        }
         cs[i] = make_float2(c * a.scale, (a.transpose ? -s : s) * a.scale);
         if (j == 0) ok[t] = p >= 0;
     }

@@ -120,6 +120,50 @@ def test_rope_into_a_view_between_its_input():
             api.csa_rope(buf[:, :bad.shape[1], :2], bad, freqs)
 
 
+def exact_turns(freq, pos):
+    """pos * freq as a fraction of a turn in [-1/2, 1/2), of 1000-bit integers (freq: a float)."""
+    one = 1 << 1000
+
+    def atan_inv(n):                                   # one * arctan(1 / n)
+        total, term, k = 0, one // n, 1
+        while term:
+            total += term // k if k % 4 == 1 else -(term // k)
+            term //= n * n
+            k += 2
+        return total
+
+    pi = 4 * (4 * atan_inv(5) - atan_inv(239))         # Machin
+    num, den = float(freq).as_integer_ratio()
+    turn = pos * num * one * one // (den * 2 * pi) % one
+    return (turn - one if 2 * turn >= one else turn) / one
+
+
+def test_rope_angles_of_large_frequencies_and_far_positions():
+    # cos and sin themselves: x = (1, 0) in every pair.  The angle is within 2^-27 of a turn (and
+    # 2^-32 where it is less than 2^-8 of a turn from a quarter turn), sincospi within 2 ulp
+    freqs = [1.0, 0.1, 3.0, 1234.5, -1234.5, 1e6, -1e6, 999999.125, 1e-3, 2.0 ** -30, 0.0, 6.283185307179586]
+    far = [0, 1, 77, 4097, 1 << 20, (1 << 24) + 1, (1 << 30) + 12345, (1 << 31) - 1]
+    f = torch.tensor(freqs, dtype=torch.float64)
+    x = torch.zeros(1, len(far), 1, 2 * len(freqs), device=DEV)
+    x[..., 0::2] = 1.0
+    got = api.rope(x, f, pos=i32([far]))[0][0, :, 0].double().cpu()
+    for t, p in enumerate(far):
+        for j, fr in enumerate(freqs):
+            turn = exact_turns(fr, p)
+            c, s = math.cos(2 * math.pi * turn), math.sin(2 * math.pi * turn)
+            for v, w in ((float(got[t, 2 * j]), c), (float(got[t, 2 * j + 1]), s)):
+                assert abs(v - w) <= 2 * math.pi * 2.0 ** -27 + 2.0 ** -22 * abs(w), (fr, p, v, w)
+    # positions whose angle is close to a quarter, half or three quarters of a turn (freq 0.01)
+    near = [p for p in range(200000) if abs((4 * p * 0.01 / (2 * math.pi)) % 1.0 - 0.5) > 0.5 - 2.0 ** -6]
+    x = torch.zeros(1, len(near), 1, 2, device=DEV)
+    x[..., 0] = 1.0
+    got = api.rope(x, torch.tensor([0.01], dtype=torch.float64), pos=i32([near]))[0][0, :, 0].double().cpu()
+    # (p * 0.01 in fp64: within 2^-42 rad of the frequency's own product)
+    ang = torch.tensor(near, dtype=torch.float64) * 0.01
+    want = torch.stack([ang.cos(), ang.sin()], 1)
+    assert float(((got - want).abs() - 2.0 ** -22 * want.abs()).max()) <= 2 * math.pi * 2.0 ** -32 + 2.0 ** -42
+
+
 def test_rope_gradient():
     # the transposed call is the gradient of the rotation: against central differences of
     # sum(w * rope(x)), which is linear in x, so a difference over any step is exact up to rounding
