@@ -26,6 +26,8 @@
 // cut in that proportion.  A unit that stays whole is written out by its CTA;
 // the parts of a cut one leave their unnormalised O (fp32), running maximum
 // and sums in the workspace, and a second kernel joins them in a fixed order.
+// Only a CTA's first and last unit can be cut, so the workspace goes with the
+// CTAs, not with the units: slot c for the first unit of CTA c, n + c for its last.
 //
 // Roles (20 warps, one CTA per SM): warps 0-1 load key tiles; warp 2 loads Q and
 // issues S = Q.K; warp 3 issues O += P.V; warps 4-11 and 12-19 turn S into P,
@@ -107,7 +109,6 @@ struct PrefixParams {
     int hshift;              // log2(H)
     int R;                   // query rows
     int U;                   // units
-    int parts;               // workspace slots per unit
     float scale_log2;
     __nv_bfloat16* out;
     float* lse;
@@ -130,7 +131,7 @@ struct RowRec {
 struct Geo {
     int P, T;
     int lo, hi;              // tiles [lo, hi)
-    int ord, whole;          // which of the unit's parts; all of the unit?
+    int whole;               // all of the unit?
 };
 constexpr size_t kSmem = 1024 + kTileBytes + kStages * kTileBytes + sizeof(Ctrl) +
                          kMaxUnits * (sizeof(Geo) + 2 * sizeof(RowRec));
@@ -190,7 +191,6 @@ __device__ __forceinline__ void fill_geometry(const PrefixParams& p, int c, int 
         const long a = (long)c * p.U, b = a + p.U, x = (long)(u0 + k) * n_cta, y = x + n_cta;
         g.lo = div_of((max(a, x) - x) * (g.P + g.T), n_cta);
         g.hi = div_of((min(b, y) - x) * (g.P + g.T), n_cta);
-        g.ord = c - div_of(x, p.U);
         g.whole = a <= x && b >= y;
         geo[k] = g;
     }
@@ -756,7 +756,7 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 }
             } else {
                 // O as [column quad][row] of float4: lanes (rows) are consecutive
-                float* ws = p.ws + (size_t)(u * p.parts + g.ord) * kPartFloats;
+                float* ws = p.ws + (size_t)(u == u0 ? c : n_cta + c) * kPartFloats;
 #pragma unroll
                 for (int e = 0; e < 32; e += 4)
                     *reinterpret_cast<float4*>(ws + ((id * 8 + (e >> 2)) * kRows + r) * 4) =
@@ -782,7 +782,8 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 }
 
 // ---------------------------------------------------------------------- join
-// A CTA per cut unit and 8 of its columns; a thread per row and share of the
+// A CTA per unit (with more units than CTAs, per border between two CTAs: each
+// lies in another unit) and 8 of its columns; a thread per row and share of the
 // parts.  What bounds it is the latency of the loads (a few parts of
 // L2-resident data): a thread's parts are fetched kBatch at a time, and where a
 // unit has many parts (few units, so few CTAs), kGroups threads share a row and
@@ -808,15 +809,16 @@ __global__ void __launch_bounds__(kGroups * kRows)
 prefix_join_kernel(const __grid_constant__ PrefixParams p, int n_cta) {
     constexpr int kPer = kD / kJoinCols;
     __shared__ float sh[kGroups > 1 ? kGroups - 1 : 1][3 + kJoinCols][kRows];
-    const int u = blockIdx.x / kPer, q0 = (blockIdx.x % kPer) * (kJoinCols / 4);
+    const int at = blockIdx.x / kPer, q0 = (blockIdx.x % kPer) * (kJoinCols / 4);
+    const int u = p.U > n_cta ? (int)((long)(at + 1) * p.U / n_cta) : at;
     const int r = threadIdx.x & (kRows - 1), grp = threadIdx.x / kRows;
     const long x = (long)u * n_cta, y = x + n_cta;
     const int c0 = (int)(x / p.U), n = (int)((y + p.U - 1) / p.U) - c0;      // the unit's parts
     grid_wait();                                                            // the parts are there
     if (n <= 1) return;                                                     // written whole
     const long orow = (long)u * kRows + r;
-    const float* ws = p.ws + (size_t)u * p.parts * kPartFloats;
-    const size_t stride = kPartFloats;
+    // the parts but the first are of their CTA's first unit
+    const int slot0 = (long)c0 * p.U == x ? c0 : n_cta + c0;
     JoinState t;
     t.m = -INFINITY;
     t.lr = t.le = 0.0f;
@@ -831,7 +833,7 @@ prefix_join_kernel(const __grid_constant__ PrefixParams p, int n_cta) {
             const int k = k0 + j * kGroups;
             m[j] = -INFINITY;
             if (k >= n) continue;
-            const float* part = ws + k * stride;
+            const float* part = p.ws + (size_t)(k == 0 ? slot0 : c0 + k) * kPartFloats;
             m[j] = part[kRows * kD + r];
             lr[j] = part[kRows * kD + kRows + r];
             le[j] = part[kRows * kD + 2 * kRows + r];
@@ -921,7 +923,7 @@ bool make_map_prefix(CUtensorMap* m, const void* ptr, uint64_t rows) {
 
 // Units and CTAs of a call, from its sizes alone.
 struct Plan {
-    int R, U, n_cta, parts;
+    int R, U, n_cta, parts;              // parts of a unit, at most
 };
 Plan plan_of(const AttnArgs& a) {
     Plan p;
@@ -956,7 +958,8 @@ bool attention_prefix_tc_supported(const AttnArgs& a) {
 unsigned long long attention_prefix_tc_workspace(const AttnArgs& a) {
     const Plan pl = plan_of(a);
     if (pl.n_cta <= pl.U && pl.U % pl.n_cta == 0) return 0;          // no unit is cut
-    return (unsigned long long)pl.U * pl.parts * kPartFloats * sizeof(float);
+    // (every unit cut alike: no CTA has two)
+    return (unsigned long long)pl.n_cta * (pl.n_cta % pl.U ? 2 : 1) * kPartFloats * sizeof(float);
 }
 
 cudaError_t launch_attention_prefix_tc(const AttnArgs& a, void* workspace, uint32_t* err, cudaStream_t s) {
@@ -977,7 +980,6 @@ cudaError_t launch_attention_prefix_tc(const AttnArgs& a, void* workspace, uint3
     p.hshift = a.H == 64 ? 6 : 7;
     p.R = pl.R;
     p.U = pl.U;
-    p.parts = pl.parts;
     p.scale_log2 = a.scale * kLog2e;
     p.out = static_cast<__nv_bfloat16*>(a.out);
     p.lse = a.lse_out;
@@ -999,7 +1001,7 @@ cudaError_t launch_attention_prefix_tc(const AttnArgs& a, void* workspace, uint3
     // after the other.  Triggered early, its waiting CTAs cost the call 6 us.  With four
     // threads a row throughout, one CTA fills an SM, and 101 units of 2 to 3 parts took
     // 20 us.)
-    const unsigned grid = (unsigned)(pl.U * (kD / kJoinCols));
+    const unsigned grid = (unsigned)((pl.U > pl.n_cta ? pl.n_cta - 1 : pl.U) * (kD / kJoinCols));
     const unsigned threads = pl.parts > 5 ? 4 * kRows : kRows;
     const auto join = pl.parts > 5 ? (lse ? prefix_join_kernel<true, 4, 5> : prefix_join_kernel<false, 4, 5>)
                                    : (lse ? prefix_join_kernel<true, 1, 3> : prefix_join_kernel<false, 1, 3>);

@@ -813,6 +813,20 @@ def test_prefix_workspace():
         run_prefix(a, workspace=ws[::2])
 
 
+@pytest.mark.parametrize("B,H,Np", [(2, 128, 5000), (70, 64, 700), (201, 64, 1000), (310, 64, 140), (301, 128, 300)])
+def test_prefix_writes_its_workspace_alone(B, H, Np):
+    # uneven and even cuts, more units than CTAs: parts at both ends of a CTA's run
+    a = prefix_case(140 + B, BF, B, 1, H, 128, Np, 30, 100)
+    need = api.load().hca_dense_attn_prefix_workspace(api.DT_BF16, B, 1, H, 128, Np, 30, 100)
+    assert need > 0
+    ws = torch.full((need + 4096,), 0xFF, dtype=torch.uint8, device=DEV)
+    out, lse = run_prefix(a, workspace=ws[:need])
+    assert bool((ws[need:] == 0xFF).all())
+    want, wl, bound, bl = ref.prefix_attention(a, BF, BF)
+    within(out, want, bound, "prefix attention")
+    within(lse, wl, bl, "lse")
+
+
 def test_timeouts_are_reported_and_the_next_call_runs_clean():
     lib = api.load()
     a, w = prefix_case(67, BF, 70, 1, 64, 128, 700, 30, 100, m=4), weights_case(68, BF, 3, 2, 64, 128, 500)

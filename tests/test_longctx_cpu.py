@@ -177,6 +177,16 @@ def test_prefix_validation(lib):
     assert lib.hca_dense_attn_prefix_workspace(1, 2, 1, 64, 128, -1, 10, 16) == 0
 
 
+def test_prefix_workspace_goes_with_the_cuts(lib):
+    # a CTA leaves two cut parts at most: a prompt of many query rows needs no more than its CTAs do
+    size = lambda B, n_q, H: lib.hca_dense_attn_prefix_workspace(1, B, n_q, H, 128, 4096, 100, 128)  # noqa: E731
+    part = (128 * 128 + 3 * 128) * 4
+    assert 0 < size(1, 1, 64) <= 148 * part
+    for B, n_q, H in ((67, 3, 64), (2, 1000, 64), (2, 8192, 64), (4, 2048, 128), (1, 16383, 64)):
+        units = (B * n_q * H + 127) // 128
+        assert 0 < size(B, n_q, H) <= 2 * max(148, (units + 29) // 30) * part, (B, n_q, H)
+
+
 def test_weights_and_evict_validation(lib):
     #       q    dt B  nq H   D    kv    N   idx   k  ne    m  pos   s    lse   in    out   stream
     ok = [FAKE, 1, 2, 1, 64, 128, FAKE, 50, FAKE, 5, None, 4, None, 0.0, FAKE, None, FAKE, None]
