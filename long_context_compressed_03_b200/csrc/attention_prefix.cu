@@ -40,8 +40,9 @@
 // The offset.  The weights are exp2(z - m) with m the row's score of one key of
 // the part's first tile, not a maximum: the true maximum is not below it, so
 // nothing that counts underflows, and fp32 sums and bf16 weights lose nothing
-// while z - m stays below 64.  Where a sum of weights reaches 2^64, the part is
-// run again: once for the rows' maxima alone, once with those as m.
+// while z - m stays below 64.  Where a sum of weights reaches 2^64, or that one
+// score is not finite, the part is run again: once for the rows' maxima alone, once
+// with those as m.
 // P has bf16's 8 significant bits (A and B of an MMA share their type, and the
 // keys are bf16): its rounding moves an output by at most 2^-8 of the spread of
 // the averaged values, like the rounding of the output itself.  The output
@@ -641,8 +642,11 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                             if (leads && h == 0) {
                                 const int c0 = i < g.P ? 0 : grp * H;
                                 float z = tmem_ld1(my + buf * 128 + c0) * p.scale_log2;
+                                const bool some = i < g.P || own_len > (i - g.P) * H;
+                                // (a score below fp32's range says nothing about the others)
+                                large |= row.on && some && !(fabsf(z) < INFINITY);
                                 if (!(fabsf(z) < INFINITY)) z = 0.0f;
-                                if (i >= g.P && own_len <= (i - g.P) * H) z = -INFINITY;
+                                if (!some) z = -INFINITY;
                                 offset[r] = z;
                                 __syncwarp();
                                 if (lane == 0) mbar_arrive(&ctl->m_ready);

@@ -418,6 +418,25 @@ def test_prefix_defaults_scale_and_large_scores(H):
     check_prefix(a, BF, softmax_scale=0.5)
 
 
+@pytest.mark.parametrize("H,nq", [(64, 1), (128, 1), (64, 2)])
+@pytest.mark.parametrize("Np", [100, 700])
+def test_prefix_first_key_of_the_lowest_value(H, nq, Np):
+    # the first key's score is below fp32's range (a masked entry of the type's lowest value), all
+    # the others' are 2^-196 in weight against a score of 0
+    a = prefix_case(98, BF, 3, nq, H, 128, Np, 20, 30)
+    a["n_entries"], a["q_pos"] = i32([Np + 20, Np + 7, Np]), (i32([[4 * Np + 100 + j for j in range(nq)]] * 3)).contiguous()
+    a["raw_pos0"] = (a["q_pos"][:, -1] - (a["kv_raw"].shape[1] - 1)).contiguous()
+    a["q"] = a["q"] * 0.125
+    for k in ("kv_p", "kv_c", "kv_raw"):
+        a[k] = a[k] * 0.125
+        a[k][..., 5:7] = torch.tensor([0.0, -48.0], device=DEV, dtype=BF)
+    a["q"][..., 5:7] = torch.tensor([4.0, 32.0], device=DEV, dtype=BF)
+    a["kv_p"][0] = 0.0
+    a["kv_p"][0, 5] = -3e38
+    a["kv_raw"][1, 0] = a["kv_p"][0]                       # (own tiles begin with the window)
+    check_prefix(a, BF)
+
+
 def test_prefix_matches_dense_call_on_the_whole_cache():
     a = prefix_case(21, BF, 6, 1, 64, 128, 900, 60, 128, m=128)
     out, lse = run_prefix(a)
