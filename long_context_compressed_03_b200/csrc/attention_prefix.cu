@@ -937,8 +937,13 @@ Plan plan_of(const AttnArgs& a) {
     // a unit's tiles, at most: shared and own
     const long own = (std::min<long>(kBN, a.N_p) + a.N_cap + a.window + a.H - 1) / a.H;
     const long T = std::max<long>(a.N_p / kBN + own, 1);
-    if (p.U >= kSms) {
-        p.n_cta = std::max(kSms, (p.U + kMaxUnits - 3) / (kMaxUnits - 2));
+    if (p.U > kSms * (kMaxUnits - 2)) {
+        // several waves: whole units for every CTA (those behind the last row are empty), so
+        // no parts to join, and no workspace that grows with the rows
+        p.n_cta = (p.U + kSms * (kMaxUnits - 2) - 1) / (kSms * (kMaxUnits - 2)) * kSms;
+        p.U = (p.U + p.n_cta - 1) / p.n_cta * p.n_cta;
+    } else if (p.U >= kSms) {
+        p.n_cta = kSms;
     } else {
         // as many whole cuts of every unit as fit one wave, no cut below one
         // tile; or an uneven cut over all SMs, whose CTAs meet two units and

@@ -749,6 +749,20 @@ def test_prefix_units_that_follow_one_another_keep_their_offsets(H, Np):
         out, lse = run_prefix(a)
 
 
+@pytest.mark.parametrize("B,nq,H", [(4440, 1, 128), (4441, 1, 128), (8881, 1, 64), (3, 3001, 64), (9000, 1, 128)])
+def test_prefix_of_more_rows_than_a_wave_takes(B, nq, H):
+    # 30 units a CTA at most; one more: two waves of whole units, the last of them empty
+    a = prefix_case(99, BF, B, nq, H, 128, 130, 2, 3, m=4, void=(B - 2,))
+    out, lse = run_prefix(a)
+    for b in sorted({0, 1, B // 2, B - 2, B - 1}):
+        j = slice(max(0, nq - 40), nq)
+        one = {k: (v[b:b + 1] if isinstance(v, torch.Tensor) and k != "kv_p" else v) for k, v in a.items()}
+        one["q"], one["q_pos"] = one["q"][:, j], one["q_pos"][:, j]
+        want, wl, bound, bl = ref.prefix_attention(one, BF, BF)
+        within(out[b:b + 1, j], want, bound, f"element {b}")
+        within(lse[b:b + 1, j], wl, bl, f"lse of element {b}")
+
+
 def test_offsets_past_32_bits():
     # caches and heads whose last rows lie more than 2^31 elements in
     g, B, N = gen(64), 5, 4_000_000

@@ -183,8 +183,8 @@ def test_prefix_workspace_goes_with_the_cuts(lib):
     part = (128 * 128 + 3 * 128) * 4
     assert 0 < size(1, 1, 64) <= 148 * part
     for B, n_q, H in ((67, 3, 64), (2, 1000, 64), (2, 8192, 64), (4, 2048, 128), (1, 16383, 64)):
-        units = (B * n_q * H + 127) // 128
-        assert 0 < size(B, n_q, H) <= 2 * max(148, (units + 29) // 30) * part, (B, n_q, H)
+        assert size(B, n_q, H) <= 2 * 148 * part, (B, n_q, H)
+    assert size(67, 3, 64) > 0 and size(2, 8192, 64) == 0  # (many rows: whole units a CTA, nothing to join)
 
 
 def test_weights_and_evict_validation(lib):
