@@ -667,9 +667,12 @@ def _weights(q, kv_c, m, lse, out, weight_in, idx, n_entries, q_pos, softmax_sca
         raise ValueError("q and kv_c must share one dtype")
     N_cap = kv_c.shape[1]
     topk = 0 if idx is None else idx.shape[-1]
+    listed = _shape(idx, (B, topk), "idx", dev, i32)
+    if idx is not None and topk == 0:
+        listed = out                               # (an empty tensor has no address, and NULL means every entry)
     _check(load().hca_entry_weights(
         _shape(q, q.shape, "q", dev), _dt(q), B, n_q, H, D, _shape(kv_c, (B, N_cap, D), "kv_c", dev), N_cap,
-        _shape(idx, (B, topk), "idx", dev, i32), topk, _shape(n_entries, (B,), "n_entries", dev, i32), m,
+        listed, topk, _shape(n_entries, (B,), "n_entries", dev, i32), m,
         _shape(q_pos, (B, n_q), "q_pos", dev, i32), softmax_scale, _shape(lse, (B, n_q, H), "lse", dev, f32),
         _shape(weight_in, (B, N_cap), "weight_in", dev, f32), out, _stream(stream)))
 

@@ -516,6 +516,19 @@ def test_entry_weights_masks_lists_and_poison(dt):
     assert torch.equal(w, run_weights(a))
 
 
+@pytest.mark.parametrize("dt,H,D", [(BF, 64, 128), (BF, 16, 64), (F32, 8, 64)])
+def test_entry_weights_of_empty_lists_and_no_rows(dt, H, D):
+    a = weights_case(73, dt, 3, 2, H, D, 70, m=1)
+    none = torch.empty(3, 0, dtype=torch.int32, device=DEV)
+    assert torch.equal(run_weights(dict(a, idx=none)), a["weight"])        # an empty list: no entry, not every one
+    assert float(run_weights(dict(a, idx=none, weight=None)).abs().max()) == 0
+    rows = dict(a, q=a["q"][:, :0], lse=a["lse"][:, :0].contiguous(), q_pos=a["q_pos"][:, :0].contiguous())
+    assert torch.equal(run_weights(rows), a["weight"])
+    idx, kept = api.evict(a["weight"].clone(), 0)                          # a budget of none, and what follows it
+    assert idx.shape == (3, 0) and int(kept.abs().max()) == 0
+    assert torch.equal(run_weights(dict(a, idx=idx)), a["weight"])
+
+
 def test_entry_weights_of_an_attention_call_sum_to_its_heads():
     # with the call's own lse and no window, every head's weights add to one
     g, B, N, H = gen(13), 3, 900, 64
