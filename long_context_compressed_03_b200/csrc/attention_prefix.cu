@@ -733,6 +733,8 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     l_e += ctl->xl[(k - 1) & 1][q][1][r];
                 }
                 m = offset[r];
+                // keys whose scores are all NaN have no maximum, but are not no keys
+                if (m == -INFINITY && l_r != 0.0f) m = 0.0f;
             }
             if (!row.on) {               // no position: no key, whatever the shared tiles held
                 m = -INFINITY;

@@ -407,6 +407,23 @@ def test_attention_from_several_host_threads():
     assert all(torch.equal(c[2], c[4]) for c in calls)
 
 
+@pytest.mark.parametrize("H,B", [(64, 1), (64, 2), (128, 1), (128, 30)])
+@pytest.mark.parametrize("value", [math.nan, -math.inf])
+def test_prefix_a_part_of_nothing_but_nan(H, B, value):
+    # the last key, alone in its tile, gives every score NaN; cut units leave it a part of its own
+    a = prefix_case(89, BF, B, 1, H, 128, 385, 0, 0)
+    a["n_entries"], a["q_pos"] = i32([385] * B), i32([[4 * 385]] * B)
+    a["kv_p"][384] = value
+    out, lse = run_prefix(a)
+    assert bool(torch.isnan(out).all()) and bool(torch.isnan(lse).all())
+    a["n_entries"][0] = 384                                # element 0 does not see it
+    out, lse = run_prefix(a)
+    want, wl, bound, bl = ref.prefix_attention(a, BF, BF)
+    within(out[0], want[0], bound[0], "element 0")
+    within(lse[0], wl[0], bl[0], "lse of element 0")
+    assert bool(torch.isnan(out[1:]).all()) and bool(torch.isnan(lse[1:]).all())
+
+
 @pytest.mark.parametrize("H", [64, 128])
 def test_prefix_defaults_scale_and_large_scores(H):
     # no optional arrays (positions 0 .. n_q - 1: a prefill over a prefix of m = 1 entries), a given
