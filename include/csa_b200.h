@@ -437,8 +437,8 @@ csa_status_t hca_dense_attn_at(const void* q, int dt, int B, int n_q, int H, int
  *     an attention output is turned back by the query's position).
  * The other channels are passed on unchanged.  A token with a negative
  * position has no place in the sequence: its heads are passed on unrotated.
- * Rotation runs in fp32 from angles within 2^-27 of a turn of p * freqs[j], at any
- * position and for any frequency allowed, and is rounded once.
+ * Rotation runs in fp32 from angles within 2^-27 of a turn of p * freqs[j], for any
+ * position below 2^31 and any frequency allowed, and is rounded once.
  *
  *   x, y   up to two tensors with D channels a head, H and H_y heads a token
  *          (query heads and the KV row, say), rotated in one launch; H or H_y
@@ -491,7 +491,11 @@ csa_status_t csa_rope_freqs(int d_rot, double base, double factor, int original_
  *                                    kv_c[b, i - N_p]   for N_p <= i < N_p + N_cap;
  *   n_entries [B] counts logical entries, prefix included (NULL: N_p + N_cap).
  * The result is that of hca_dense_attn over the logical caches (the serving
- * counterpart of "DS-V4 分析&学习" §1.4; sharing is this library's addition).
+ * counterpart of "DS-V4 分析&学习" §1.4; sharing is this library's addition), up to
+ * rounding: bf16 calls round the softmax weights to bf16 (as the calls with q_pos do;
+ * hca_dense_attn without it keeps 11 bits), which moves an output by at most 2^-8 of
+ * the spread of the values it averages, and the LSE not at all.  A key that is not
+ * finite enters the rows that see it and no others.
  *   kv_p  [N_p, D]   kv_c  [B, N_cap, D]   (either may have no rows)
  *   workspace  device memory of at least hca_dense_attn_prefix_workspace(...)
  *     bytes, on a 16-byte boundary (may be NULL where that is 0).  Its contents
@@ -533,7 +537,8 @@ csa_status_t hca_dense_attn_prefix(const void* q, int dt, int B, int n_q, int H,
  *   lse [B, n_q, H] fp32;  q_pos [B, n_q] (NULL: q);  n_entries [B] (NULL: N_cap).
  *   weight_in [B, N_cap] fp32 or NULL (zeros); it may be weight_out, and must not
  *     overlap it otherwise.  weight_out [B, N_cap] fp32.
- *   Products and sums are fp32.  softmax_scale <= 0 selects 1/sqrt(D).
+ *   Products and sums are fp32, exponentials within 2^-22 (below 2^-126: 0).
+ *   softmax_scale <= 0 selects 1/sqrt(D).
  *   Limits: D a multiple of 16 and <= 256, H >= 1.
  */
 csa_status_t hca_entry_weights(const void* q, int dt, int B, int n_q, int H, int D,

@@ -128,6 +128,8 @@ constexpr int kMmaThreads = kMmaWarps * 32;
 constexpr int kMmaKeys = 32 * kMmaWarps;      // keys a CTA
 constexpr int kCols = 64;                     // (query row, head) columns a step
 
+// 2^x within 2^-22 of itself, results below 2^-126 as 0: the scores' own rounding (D products
+// in fp32) moves a weight by more.
 __device__ __forceinline__ float wex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

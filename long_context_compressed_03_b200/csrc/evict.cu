@@ -299,7 +299,8 @@ __global__ void __launch_bounds__(NT) evict_regs_kernel(EvictArgs a) {
 }  // namespace
 
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s) {
-    // in registers where a CTA of 256 or 1024 threads holds the entries
+    // in registers where a CTA of 256 or 1024 threads holds the entries (64 x 32768 to 2048: 16
+    // us; 64 x 65536 by the kernel that reads them again for every digit: 87 us, 39 once cut)
     cudaError_t e = cudaSuccess;
     if (a.N_cap <= 256 * 16) e = launch_dependent(evict_regs_kernel<256, 16>, (unsigned)a.B, 256, 0, s, a);
     else if (a.N_cap <= 1024 * 32) e = launch_dependent(evict_regs_kernel<1024, 32>, (unsigned)a.B, 1024, 0, s, a);
